@@ -6,7 +6,7 @@ forward and backward, neither of which keeps the [T, V] logits:
   logp     log-probability of each token's target under softmax(logit_scale * hidden @ weight^T), and the
            log-sum-exp it was normalised with; a token whose target is negative is left out (0, 0).
   distill  cross entropy to a teacher's top entries, as a KL divergence: the teacher's given logits are
-           softmax-ed over the entries present (id >= 0, logit above -inf), the student over the whole
+           softmax-ed over the entries present (id >= 0, logit not -inf), the student over the whole
            vocabulary; a token without entries is left out (0, 0).
 
 `own` selects what run() does: False, the plain form (32-bit torch operations, rounded once at the end);
@@ -139,7 +139,7 @@ def _run_own(s):
 def _teacher(s):
     """(present entries, their ids, the teacher's probabilities over them, tokens with any)."""
     ids, u = s["teacher_ids"].long(), s["teacher_logits"] * s["scale"]
-    there = (ids >= 0) & (u > -math.inf)
+    there = (ids >= 0) & (u != -math.inf)
     some = there.any(1)
     u = torch.where(there, u, -math.inf)
     e = torch.exp(u - torch.where(some, u.amax(1), 0.0)[:, None])
@@ -170,7 +170,7 @@ def _run_plain(s):
         y = z.gather(1, target[:, None])[:, 0] - lse
         return {"logp": torch.where(some, y, 0.0), "lse": torch.where(some, lse, 0.0)}
     log_q = z.gather(1, ids) - lse[:, None]
-    term = torch.where(there & (p > 0), p * (torch.log(p) - log_q), 0.0)
+    term = torch.where(there & (p != 0), p * (torch.log(p) - log_q), 0.0)
     return {"loss": torch.where(some, term.sum(1), 0.0), "lse": torch.where(some, lse, 0.0)}
 
 
