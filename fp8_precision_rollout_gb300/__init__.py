@@ -13,6 +13,8 @@ from .binding import (  # noqa: F401
     Fp8rlError,
     decode_attention_fp8kv,
     device_status,
+    distill_topk,
+    distill_topk_backward,
     gemm_w8a8_blockwise,
     inject_device_status,
     grouped_gemm_w8a8_blockwise,
@@ -31,7 +33,10 @@ from .binding import (  # noqa: F401
     silu_mul_bf16,
     silu_mul_quantize,
     tis_weights,
+    token_logprobs,
+    token_logprobs_backward,
     version,
+    vocab_workspace_bytes,
     weight_shard_rows,
 )
 from . import weight_sync  # noqa: F401

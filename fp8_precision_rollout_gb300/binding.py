@@ -79,6 +79,15 @@ def load(path: Optional[str] = None):
                                                     ctypes.c_size_t, P]),
         "fp8rl_decode_attention_fp8kv": (ctypes.c_int, [P, P, P, P, P, P, P, i32, i32, i32, i32,
                                                         i32, i32, i32, f32, P, P]),
+        "fp8rl_vocab_workspace_bytes": (ctypes.c_size_t, [i64, i64, i64, i32, i32]),
+        "fp8rl_token_logprobs": (ctypes.c_int, [P, i64, P, i64, P, i64, i64, i64, f32, P, P, P,
+                                                ctypes.c_size_t, P]),
+        "fp8rl_token_logprobs_backward": (ctypes.c_int, [P, i64, P, i64, P, P, P, i64, i64, i64,
+                                                         f32, P, P, P, ctypes.c_size_t, P]),
+        "fp8rl_distill_topk": (ctypes.c_int, [P, i64, P, i64, P, P, i32, i64, i64, i64, f32, P, P,
+                                              P, ctypes.c_size_t, P]),
+        "fp8rl_distill_topk_backward": (ctypes.c_int, [P, i64, P, i64, P, P, i32, P, P, i64, i64,
+                                                       i64, f32, P, P, P, ctypes.c_size_t, P]),
         "fp8rl_device_status": (ctypes.c_int, [i32, i32]),
         "fp8rl_weight_shard_rows": (ctypes.c_int, [i64, i32, i32, P, P]),
         "fp8rl_inject_device_status": (ctypes.c_int, [i32, ctypes.c_uint32, ctypes.c_uint32]),
@@ -488,6 +497,165 @@ def is_weights_stats_loss(logp_train, logp_rollout, loss, mask=None, c_hi: float
     statistic (sum of fl32(w * loss) over the valid tokens)."""
     return is_weights_stats(logp_train, logp_rollout, mask, c_hi, c_lo, mode, w, stats, weights,
                             stream, loss=loss)
+
+
+# -------------------------------------------------------- vocabulary head --
+
+def vocab_workspace_bytes(tokens: int, hidden_dim: int, vocab: int, top_k: int = 0,
+                          backward: bool = False) -> int:
+    """Workspace bytes of token_logprobs / distill_topk (top_k > 0) and their
+    backward calls; 0 for sizes they do not support."""
+    return int(load().fp8rl_vocab_workspace_bytes(int(tokens), int(hidden_dim), int(vocab),
+                                                  int(top_k), 1 if backward else 0))
+
+
+def _head(hidden, weight):
+    _rowmajor(_dev(hidden, torch.bfloat16, "hidden"), "hidden")
+    _rowmajor(_dev(weight, torch.bfloat16, "weight"), "weight")
+    if hidden.shape[1] != weight.shape[1]:
+        raise ValueError("hidden [tokens, hidden_dim] and weight [vocab, hidden_dim] must agree")
+    return hidden.shape[0], hidden.shape[1], weight.shape[0]
+
+
+def _row_stride(t):
+    # the stride of a single row says nothing (torch may report any value)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _dense(t, dtype, shape, like, name):
+    _dev(t, dtype, name)
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != like.device:
+        raise ValueError("%s must be a dense %s tensor on %s" % (name, list(shape), like.device))
+    return t
+
+
+def _head_workspace(workspace, t, h, v, k, backward, like, stream):
+    if workspace is None:
+        workspace = torch.empty(max(1, vocab_workspace_bytes(t, h, v, k, backward)),
+                                dtype=torch.uint8, device=like.device)
+        if stream != torch.cuda.current_stream(like.device).cuda_stream:
+            # freed on return: the allocator must know the stream that still uses it
+            workspace.record_stream(torch.cuda.ExternalStream(stream, device=like.device))
+    _dev(workspace, torch.uint8, "workspace")
+    if not workspace.is_contiguous() or workspace.device != like.device:
+        raise ValueError("workspace must be a contiguous tensor on %s" % like.device)
+    return workspace
+
+
+def _teacher_entries(teacher_ids, teacher_logits, t, like):
+    _dev(teacher_ids, torch.int32, "teacher_ids")
+    if teacher_ids.dim() != 2:
+        raise ValueError("teacher_ids must be [tokens, top_k]")
+    k = teacher_ids.shape[1]
+    _dense(teacher_ids, torch.int32, (t, k), like, "teacher_ids")
+    _dense(teacher_logits, torch.float32, (t, k), like, "teacher_logits")
+    return k
+
+
+def token_logprobs(hidden, weight, targets, logit_scale: float = 1.0,
+                   logp: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None):
+    """Log-probability of targets int32 [T] under softmax(logit_scale * hidden @ weight^T)
+    (bf16 hidden [T, H], weight [V, H]) and the log-sum-exp, float32 [T] each:
+    (logp, lse).  Tokens with a negative target are left out (0, 0)."""
+    t, h, v = _head(hidden, weight)
+    _dense(targets, torch.int32, (t,), hidden, "targets")
+    if logp is None:
+        logp = torch.empty(t, dtype=torch.float32, device=hidden.device)
+    if lse is None:
+        lse = torch.empty(t, dtype=torch.float32, device=hidden.device)
+    _dense(logp, torch.float32, (t,), hidden, "logp")
+    _dense(lse, torch.float32, (t,), hidden, "lse")
+    s = _stream(stream)
+    ws = _head_workspace(workspace, t, h, v, 0, False, hidden, s)
+    _check(load().fp8rl_token_logprobs(hidden.data_ptr(), _row_stride(hidden), weight.data_ptr(),
+                                       _row_stride(weight), targets.data_ptr(), t, h, v,
+                                       float(logit_scale), logp.data_ptr(), lse.data_ptr(),
+                                       ws.data_ptr(), ws.numel(), s))
+    return logp, lse
+
+
+def _head_gradients(hidden, weight, grad_hidden, grad_weight, need_hidden, need_weight):
+    t, h, v = hidden.shape[0], hidden.shape[1], weight.shape[0]
+    if grad_hidden is None and need_hidden:
+        grad_hidden = torch.empty(t, h, dtype=torch.bfloat16, device=hidden.device)
+    if grad_weight is None and need_weight:
+        grad_weight = torch.empty(v, h, dtype=torch.bfloat16, device=hidden.device)
+    if grad_hidden is not None:
+        _dense(grad_hidden, torch.bfloat16, (t, h), hidden, "grad_hidden")
+    if grad_weight is not None:
+        _dense(grad_weight, torch.bfloat16, (v, h), hidden, "grad_weight")
+    return grad_hidden, grad_weight
+
+
+def token_logprobs_backward(hidden, weight, targets, lse, grad_logp, logit_scale: float = 1.0,
+                            grad_hidden: Optional[torch.Tensor] = None,
+                            grad_weight: Optional[torch.Tensor] = None, need_hidden: bool = True,
+                            need_weight: bool = True, workspace: Optional[torch.Tensor] = None,
+                            stream=None):
+    """Gradients (bf16 grad_hidden [T, H], grad_weight [V, H]) of
+    sum(grad_logp * logp), with the lse token_logprobs returned.  An output
+    that is neither given nor needed is not computed (None)."""
+    t, h, v = _head(hidden, weight)
+    _dense(targets, torch.int32, (t,), hidden, "targets")
+    _dense(lse, torch.float32, (t,), hidden, "lse")
+    _dense(grad_logp, torch.float32, (t,), hidden, "grad_logp")
+    gh, gw = _head_gradients(hidden, weight, grad_hidden, grad_weight, need_hidden, need_weight)
+    s = _stream(stream)
+    ws = _head_workspace(workspace, t, h, v, 0, True, hidden, s)
+    _check(load().fp8rl_token_logprobs_backward(
+        hidden.data_ptr(), _row_stride(hidden), weight.data_ptr(), _row_stride(weight),
+        targets.data_ptr(), lse.data_ptr(), grad_logp.data_ptr(), t, h, v, float(logit_scale),
+        gh.data_ptr() if gh is not None else None, gw.data_ptr() if gw is not None else None,
+        ws.data_ptr(), ws.numel(), s))
+    return gh, gw
+
+
+def distill_topk(hidden, weight, teacher_ids, teacher_logits, logit_scale: float = 1.0,
+                 loss: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, stream=None):
+    """KL divergence (float32 [T]) from the teacher's top entries (teacher_ids
+    int32 [T, K], teacher_logits float32 [T, K]; id < 0 or logit -inf: absent)
+    to the student softmax(logit_scale * hidden @ weight^T), and the student's
+    log-sum-exp: (loss, lse).  Tokens without entries are left out (0, 0)."""
+    t, h, v = _head(hidden, weight)
+    k = _teacher_entries(teacher_ids, teacher_logits, t, hidden)
+    if loss is None:
+        loss = torch.empty(t, dtype=torch.float32, device=hidden.device)
+    if lse is None:
+        lse = torch.empty(t, dtype=torch.float32, device=hidden.device)
+    _dense(loss, torch.float32, (t,), hidden, "loss")
+    _dense(lse, torch.float32, (t,), hidden, "lse")
+    s = _stream(stream)
+    ws = _head_workspace(workspace, t, h, v, k, False, hidden, s)
+    _check(load().fp8rl_distill_topk(hidden.data_ptr(), _row_stride(hidden), weight.data_ptr(),
+                                     _row_stride(weight), teacher_ids.data_ptr(),
+                                     teacher_logits.data_ptr(), k, t, h, v, float(logit_scale),
+                                     loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), s))
+    return loss, lse
+
+
+def distill_topk_backward(hidden, weight, teacher_ids, teacher_logits, lse, grad_loss,
+                          logit_scale: float = 1.0, grad_hidden: Optional[torch.Tensor] = None,
+                          grad_weight: Optional[torch.Tensor] = None, need_hidden: bool = True,
+                          need_weight: bool = True, workspace: Optional[torch.Tensor] = None,
+                          stream=None):
+    """Gradients (bf16 grad_hidden [T, H], grad_weight [V, H]) of
+    sum(grad_loss * loss), with the lse distill_topk returned; outputs as in
+    token_logprobs_backward."""
+    t, h, v = _head(hidden, weight)
+    k = _teacher_entries(teacher_ids, teacher_logits, t, hidden)
+    _dense(lse, torch.float32, (t,), hidden, "lse")
+    _dense(grad_loss, torch.float32, (t,), hidden, "grad_loss")
+    gh, gw = _head_gradients(hidden, weight, grad_hidden, grad_weight, need_hidden, need_weight)
+    s = _stream(stream)
+    ws = _head_workspace(workspace, t, h, v, k, True, hidden, s)
+    _check(load().fp8rl_distill_topk_backward(
+        hidden.data_ptr(), _row_stride(hidden), weight.data_ptr(), _row_stride(weight),
+        teacher_ids.data_ptr(), teacher_logits.data_ptr(), k, lse.data_ptr(), grad_loss.data_ptr(),
+        t, h, v, float(logit_scale), gh.data_ptr() if gh is not None else None,
+        gw.data_ptr() if gw is not None else None, ws.data_ptr(), ws.numel(), s))
+    return gh, gw
 
 
 def quantize_kv_fp8_calibrate_noalloc(x: torch.Tensor, scales: Optional[torch.Tensor] = None,

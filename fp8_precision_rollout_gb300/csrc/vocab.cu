@@ -1,0 +1,619 @@
+// vocab.cu -- token log-probabilities and top-k distillation over a language
+// model's vocabulary, forward and backward, without the [tokens, vocab] logits.
+//
+// FP8-RL summary, section 3.4.3: the importance weight exp(logp_train -
+// logp_rollout) needs each token's log-probability under the training policy.
+// With hidden states h_t, vocabulary rows w_v and z_tv = scale * <h_t, w_v>:
+//
+//   lse_t  = log sum_v exp z_tv            logp_t = z_ty - lse_t
+//   loss_t = sum_k p_tk (log p_tk - (z_t,id_k - lse_t))   p = softmax of the
+//            teacher's entries (distillation; the p_tk of a token sum to 1)
+//   d logp_t / d z_tv = [v = y] - q_tv     d loss_t / d z_tv = q_tv - p_tv
+//   q_tv = exp(z_tv - lse_t)
+//
+// so both are a sparse target distribution against the full softmax, and both
+// gradients are G = g_t * scale * (+-)(q - target) followed by dH = G W and
+// dW = G^T H.  One call runs
+//   teacher_kernel   (distillation) softmax of each token's entries, entries
+//                    sorted by id so that an epilogue finds a column range's
+//                    entries by bisection;
+//   rows_kernel      packs the tokens that have a target into consecutive
+//                    rows: a left-out token costs no products, and what its
+//                    hidden state holds (NaN included) reaches nothing;
+//   the products     (vocab_gemm.cu), over pieces of the vocabulary;
+//   combine_kernel / scatter_kernel   outputs per token.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "vocab.h"
+
+namespace fp8rl {
+namespace {
+
+constexpr int kMaxTopK = 256;
+constexpr int kRowThreads = 256;
+constexpr int kTeacherWarps = 4;
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// One warp per token.  An entry is present if its id is in [0, V) and its
+// scaled logit is not -inf; NaN stays in the softmax and makes the row NaN.
+// Writes the entries in ascending id order (absent ones last, id INT_MAX,
+// p 0), and flags[t] = 0, or -1 for a token without entries.
+__global__ void __launch_bounds__(kTeacherWarps * 32)
+    teacher_kernel(const int32_t* ids, const float* logits, int64_t T, int K, int V, float scale,
+                   int32_t* ids_s, float* p_s, float* lp_s, int32_t* flags, uint32_t* status) {
+  __shared__ int32_t sid[kTeacherWarps][kMaxTopK];
+  __shared__ float su[kTeacherWarps][kMaxTopK];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)blockIdx.x * kTeacherWarps + warp;
+  if (t >= T) return;
+  int32_t* id = sid[warp];
+  float* u = su[warp];
+  float mx = -INFINITY;
+  bool any = false, bad = false;
+  for (int j = lane; j < K; j += 32) {
+    const int32_t i = ids[t * K + j];
+    const float x = logits[t * K + j] * scale;
+    bad |= i >= V;
+    const bool there = i >= 0 && i < V && x != -INFINITY;
+    id[j] = there ? i : INT_MAX;
+    u[j] = x;
+    if (there) mx = fmaxf(mx, x);
+    any |= there;
+  }
+  mx = warp_max(mx);
+  any = __any_sync(0xFFFFFFFFu, any);
+  if (bad) atomicOr(status, kStatusBadIndex);
+  __syncwarp();
+  float s = 0.0f;
+  for (int j = lane; j < K; j += 32)
+    if (id[j] != INT_MAX) s += expf(u[j] - mx);
+  s = warp_sum(s);
+  const float ls = logf(s);
+  for (int j = lane; j < K; j += 32) {
+    const int32_t mine = id[j];
+    int r = 0;
+    for (int i = 0; i < K; ++i) r += (id[i] < mine || (id[i] == mine && i < j)) ? 1 : 0;
+    const bool there = mine != INT_MAX;
+    ids_s[t * K + r] = mine;
+    p_s[t * K + r] = there ? expf(u[j] - mx) / s : 0.0f;
+    if (lp_s) lp_s[t * K + r] = there ? (u[j] - mx) - ls : 0.0f;
+  }
+  if (lane == 0) flags[t] = any ? 0 : -1;
+}
+
+struct RowsArgs {
+  const int32_t* flags;        // [T] target of each token; negative: left out
+  int64_t T;
+  int V, H, rows_per_cta;
+  const __nv_bfloat16* hidden; // [T, H], row stride ldh
+  int64_t ldh;
+  __nv_bfloat16* x;            // [rows_pad, H]
+  int32_t* map;
+  int32_t* tgt;
+  int32_t* n_rows;
+  // forward: outputs of left-out tokens (0)
+  float* out0;
+  float* out1;
+  // backward
+  const float* lse;            // [T]
+  const float* grad;           // [T]
+  float coef;                  // +-scale
+  float* lse_c;
+  float* gcoef_c;
+  __nv_bfloat16* grad_hidden;  // [T, H] rows of left-out tokens become 0, or null
+  uint32_t* status;
+};
+
+// CTA b packs tokens [b*R, (b+1)*R): it counts the kept tokens before its
+// range itself (targets are 4 bytes, a row is 2H), so CTAs do not depend on
+// one another and the order is the tokens' order.
+__global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsArgs a) {
+  __shared__ int wsum[kRowThreads / 32];
+  __shared__ int idx[kRowThreads];
+  __shared__ int sbase;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t r0 = (int64_t)blockIdx.x * a.rows_per_cta;
+  const int64_t r1 = min(a.T, r0 + a.rows_per_cta);
+  int before = 0;
+  for (int64_t i = tid; i < r0; i += kRowThreads) {
+    const int32_t f = a.flags[i];
+    before += (f >= 0 && f < a.V) ? 1 : 0;
+  }
+  before = __reduce_add_sync(0xFFFFFFFFu, before);
+  if (lane == 0) wsum[warp] = before;
+  __syncthreads();
+  if (tid == 0) {
+    int b = 0;
+    for (int w = 0; w < kRowThreads / 32; ++w) b += wsum[w];
+    sbase = b;
+  }
+  __syncthreads();
+  int base = sbase;
+  const int vecs = a.H / 8;
+  for (int64_t c0 = r0; c0 < r1; c0 += kRowThreads) {
+    const int64_t t = c0 + tid;
+    const int32_t f = t < r1 ? a.flags[t] : -1;
+    const bool keep = f >= 0 && f < a.V;
+    if (f >= a.V) atomicOr(a.status, kStatusBadIndex);
+    const unsigned bal = __ballot_sync(0xFFFFFFFFu, keep);
+    if (lane == 0) wsum[warp] = __popc(bal);
+    __syncthreads();
+    int c = base + __popc(bal & ((1u << lane) - 1u));
+    int total = 0;
+    for (int w = 0; w < kRowThreads / 32; ++w) {
+      if (w < warp) c += wsum[w];
+      total += wsum[w];
+    }
+    idx[tid] = keep ? c : -1;
+    if (keep) {
+      a.map[c] = (int32_t)t;
+      a.tgt[c] = f;
+      if (a.grad) {
+        a.lse_c[c] = a.lse[t];
+        a.gcoef_c[c] = a.grad[t] * a.coef;
+      }
+    } else if (t < r1 && a.out0) {
+      a.out0[t] = 0.0f;
+      a.out1[t] = 0.0f;
+    }
+    base += total;
+    __syncthreads();
+    const int here = (int)min((int64_t)kRowThreads, r1 - c0);
+    for (int r = warp; r < here; r += kRowThreads / 32) {
+      const int dst = idx[r];
+      if (dst >= 0) {
+        const uint4* src = reinterpret_cast<const uint4*>(a.hidden + (c0 + r) * a.ldh);
+        uint4* to = reinterpret_cast<uint4*>(a.x + (int64_t)dst * a.H);
+        for (int v = lane; v < vecs; v += 32) to[v] = __ldg(src + v);
+      } else if (a.grad_hidden) {
+        uint4* to = reinterpret_cast<uint4*>(a.grad_hidden + (c0 + r) * a.H);
+        for (int v = lane; v < vecs; v += 32) to[v] = make_uint4(0, 0, 0, 0);
+      }
+    }
+    __syncthreads();
+  }
+  if (r1 == a.T) {
+    if (tid == 0) *a.n_rows = base;
+    if (a.grad) {
+      // dW sums over rows in steps of 64: the rows that fill the last step are zero
+      const int end = (max(base, 1) + 63) / 64 * 64;
+      uint4* to = reinterpret_cast<uint4*>(a.x + (int64_t)base * a.H);
+      for (int64_t v = tid; v < (int64_t)(end - base) * vecs; v += kRowThreads)
+        to[v] = make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
+struct CombineArgs {
+  const int32_t* n_rows;
+  const int32_t* map;
+  const float2* part;
+  int parts, rows_pad, K;
+  const float* zt;
+  const float* p;
+  const float* lp;
+  float scale;
+  float* out;   // logp or loss, [T]
+  float* lse;   // [T]
+};
+
+// Joins the softmax partial (m2, r2) into (m, r): a maximum and the sum of the
+// exponentials relative to it less the maximum's own 1.  Nothing: (-inf, -1).
+__device__ __forceinline__ void join(float& m, float& r, float m2, float r2, float k2) {
+  const float d = (m2 - m) * k2;
+  if (m2 > m) {
+    r = r2 + (1.0f + r) * exp2f(-d);
+    m = m2;
+  } else if (m2 == -INFINITY) {
+    r += 1.0f + r2;               // adds nothing, or a NaN
+  } else {
+    r = r + (1.0f + r2) * exp2f(d);
+  }
+}
+
+// Joins the softmax partials of 32 rows: 32 x 32 threads, lane = row, each
+// warp takes every 32nd part; then every warp the row's entries.  All sums
+// FP32 in a fixed order.
+__global__ void __launch_bounds__(1024) combine_kernel(const CombineArgs a) {
+  __shared__ float sm[32][33], ss[32][33];
+  const int n = *a.n_rows;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  if (blockIdx.x * 32 >= n) return;
+  const float k2 = a.scale * 1.4426950408889634f;
+  const bool ok = c < n;
+  float m = -INFINITY, r = -1.0f;
+  if (ok) {
+#pragma unroll 4
+    for (int i = warp; i < a.parts; i += 32) {
+      const float2 q = a.part[(int64_t)i * a.rows_pad + c];
+      join(m, r, q.x, q.y, k2);
+    }
+  }
+  sm[warp][lane] = m;
+  ss[warp][lane] = r;
+  __syncthreads();
+  float top = -INFINITY, rest = -1.0f;
+  for (int i = 0; i < 32; ++i) join(top, rest, sm[i][lane], ss[i][lane], k2);
+  // Log-probabilities as (x - top) * scale - log(sum), the sum as 1 + rest: a
+  // nearly certain word, whose log-probability is close to -rest, keeps its
+  // relative accuracy, and a certain one has exactly 0.
+  const float ls = log1pf(rest);
+  const float lse = __fadd_rn(__fmul_rn(top, a.scale), ls);
+  __syncthreads();
+  float loss = 0.0f;
+  int64_t t = ok ? a.map[c] : 0;
+  if (ok && a.K) {
+    for (int k = warp; k < a.K; k += 32) {
+      const float p = a.p[t * a.K + k];
+      if (p != 0.0f) loss += p * (a.lp[t * a.K + k] -
+                     __fsub_rn(__fmul_rn(a.zt[(int64_t)c * a.K + k] - top, a.scale), ls));
+    }
+  }
+  sm[warp][lane] = loss;
+  __syncthreads();
+  if (warp != 0 || !ok) return;
+  a.lse[t] = lse;
+  if (a.K == 0) {
+    a.out[t] = __fsub_rn(__fmul_rn(a.zt[c] - top, a.scale), ls);
+  } else {
+    float l = 0.0f;
+    for (int i = 0; i < 32; ++i) l += sm[i][lane];
+    a.out[t] = l;
+  }
+}
+
+// dX of the compact rows (FP32) -> grad_hidden rows of their tokens.
+__global__ void __launch_bounds__(256)
+    scatter_kernel(const float* dx, const int32_t* n_rows, const int32_t* map, int H,
+                   __nv_bfloat16* grad_hidden) {
+  const int vecs = H / 8;
+  const int64_t total = (int64_t)*n_rows * vecs;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t c = i / vecs;
+    const int v = (int)(i - c * vecs);
+    const float4* src = reinterpret_cast<const float4*>(dx + c * H + v * 8);
+    const float4 x = src[0], y = src[1];
+    __nv_bfloat162 b[4] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w),
+                           __floats2bfloat162_rn(y.x, y.y), __floats2bfloat162_rn(y.z, y.w)};
+    *reinterpret_cast<uint4*>(grad_hidden + (int64_t)map[c] * H + v * 8) =
+        *reinterpret_cast<uint4*>(b);
+  }
+}
+
+// ------------------------------------------------------------------- host --
+
+// The workspace's parts, in order, each 256-byte aligned.
+struct Plan {
+  int64_t rows = 0;        // tokens handled at once (forward: a piece of them)
+  int64_t rows_pad = 0;
+  int64_t vc = 0;          // backward: vocabulary columns of a piece
+  size_t x, map, tgt, n, part, zt, lse, gcoef, g, dx, flags, ids, p, lp, bytes;
+};
+
+int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+// Forward: tokens go in pieces whose softmax partials fit kPartBytes, so the
+// workspace grows with neither tokens x vocab nor tokens beyond a piece.
+// Backward: the vocabulary goes in pieces whose G fits kGradBytes.
+constexpr int64_t kPartBytes = 128ll << 20;
+constexpr int64_t kGradBytes = 192ll << 20;
+
+Plan make_plan(int64_t T, int64_t H, int64_t V, int64_t K, bool backward) {
+  Plan pl;
+  const int64_t parts = (V + kVocabPart - 1) / kVocabPart;
+  pl.rows = T;
+  if (!backward) {
+    const int64_t most = std::max<int64_t>(2048, kPartBytes / (parts * 8) / kVocabRowPad * kVocabRowPad);
+    pl.rows = std::min(T, most);
+  }
+  pl.rows_pad = round_up(std::max<int64_t>(pl.rows, 1), kVocabRowPad);
+  size_t at = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at = (size_t)round_up((int64_t)(at + bytes), 256);
+    return here;
+  };
+  pl.x = take((size_t)pl.rows_pad * H * 2);
+  pl.map = take((size_t)pl.rows_pad * 4);
+  pl.tgt = take((size_t)pl.rows_pad * 4);
+  pl.n = take(256);
+  if (!backward) {
+    pl.part = take((size_t)pl.rows_pad * parts * 8);
+    pl.zt = take((size_t)pl.rows_pad * std::max<int64_t>(K, 1) * 4);
+  } else {
+    pl.vc = std::max<int64_t>(256, kGradBytes / (pl.rows_pad * 2) / 256 * 256);
+    pl.vc = std::min(pl.vc, round_up(V, 256));
+    pl.lse = take((size_t)pl.rows_pad * 4);
+    pl.gcoef = take((size_t)pl.rows_pad * 4);
+    pl.g = take((size_t)pl.rows_pad * pl.vc * 2);
+    pl.dx = take((size_t)pl.rows_pad * H * 4);
+  }
+  if (K) {
+    pl.flags = take((size_t)pl.rows_pad * 4);
+    pl.ids = take((size_t)pl.rows * K * 4);
+    pl.p = take((size_t)pl.rows * K * 4);
+    if (!backward) pl.lp = take((size_t)pl.rows * K * 4);
+  }
+  pl.bytes = at;
+  return pl;
+}
+
+bool shape_ok(int64_t T, int64_t H, int64_t V, int64_t K) {
+  return T >= 0 && T <= INT32_MAX / 2 && H >= 8 && H <= (1 << 20) && H % 8 == 0 && V >= 1 &&
+         V <= INT32_MAX / 2 && K >= 0 && K <= kMaxTopK;
+}
+
+struct Call {
+  const void* hidden;
+  int64_t ldh;
+  const void* weight;
+  int64_t ldw;
+  const int32_t* targets;      // K == 0
+  const int32_t* ids;          // K > 0
+  const float* logits;
+  int64_t T, H, V, K;
+  float scale;
+  float* out;                  // forward
+  float* lse_out;
+  const float* lse;            // backward
+  const float* grad;
+  void* grad_hidden;
+  void* grad_weight;
+  char* ws;
+  size_t ws_bytes;
+  cudaStream_t stream;
+};
+
+fp8rl_status check_call(const Call& c, bool backward) {
+  if (c.T < 0 || c.H < 0 || c.V < 0) return fail(FP8RL_ERR_INVALID_ARG, "negative size");
+  if (c.T > INT32_MAX / 2 || c.V < 1 || c.V > INT32_MAX / 2)
+    return fail(FP8RL_ERR_UNSUPPORTED_SHAPE, "need tokens <= 2^30 and 1 <= vocab <= 2^30");
+  if (c.H < 8 || c.H % 8 || c.H > (1 << 20))
+    return fail(FP8RL_ERR_UNSUPPORTED_SHAPE, "hidden_dim must be a multiple of 8 in [8, 2^20] (got %lld)",
+                (long long)c.H);
+  if (c.K < 0 || c.K > kMaxTopK)
+    return fail(FP8RL_ERR_UNSUPPORTED_SHAPE, "need 1 <= top_k <= %d", kMaxTopK);
+  if (!(c.scale > 0.0f) || !std::isfinite(c.scale))
+    return fail(FP8RL_ERR_INVALID_ARG, "logit_scale must be finite and positive");
+  if (c.ldh < c.H || c.ldw < c.H) return fail(FP8RL_ERR_INVALID_ARG, "row stride below hidden_dim");
+  if (c.ldh % 8 || c.ldw % 8)
+    return fail(FP8RL_ERR_ALIGNMENT, "row strides must be multiples of 8 elements");
+  if (backward && c.T > 0 && !c.grad_hidden && !c.grad_weight)
+    return fail(FP8RL_ERR_INVALID_ARG, "neither grad_hidden nor grad_weight is wanted");
+  if (!c.weight || !c.ws) return fail(FP8RL_ERR_INVALID_ARG, "null pointer");
+  if (c.T > 0) {
+    if (!c.hidden || (c.K ? !c.ids || !c.logits : !c.targets))
+      return fail(FP8RL_ERR_INVALID_ARG, "null pointer");
+    if (backward ? !c.lse || !c.grad : !c.out || !c.lse_out)
+      return fail(FP8RL_ERR_INVALID_ARG, "null pointer");
+  }
+  if (!aligned(c.hidden, 16) || !aligned(c.weight, 16) || !aligned(c.grad_hidden, 16) ||
+      !aligned(c.grad_weight, 16))
+    return fail(FP8RL_ERR_ALIGNMENT, "hidden, weight and their gradients must be 16-byte aligned");
+  if (!aligned(c.targets, 4) || !aligned(c.ids, 4) || !aligned(c.logits, 4) || !aligned(c.out, 4) ||
+      !aligned(c.lse_out, 4) || !aligned(c.lse, 4) || !aligned(c.grad, 4))
+    return fail(FP8RL_ERR_ALIGNMENT, "per-token arrays must be 4-byte aligned");
+  if (!aligned(c.ws, 256)) return fail(FP8RL_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+  const size_t need = make_plan(c.T, c.H, c.V, c.K, backward).bytes;
+  if (c.ws_bytes < need)
+    return fail(FP8RL_ERR_INVALID_ARG, "workspace has %zu bytes, %zu are needed", c.ws_bytes, need);
+  return FP8RL_OK;
+}
+
+// Teacher softmax (K > 0) and row packing of tokens [t0, t0 + rows).
+fp8rl_status pack_rows(const Call& c, const Plan& pl, const DeviceState* ds, int64_t t0,
+                       int64_t rows, bool backward, float coef, VocabArgs* va) {
+  char* ws = c.ws;
+  const int32_t* flags = c.K ? nullptr : c.targets + t0;
+  if (c.K) {
+    int32_t* f = reinterpret_cast<int32_t*>(ws + pl.flags);
+    int32_t* ids = reinterpret_cast<int32_t*>(ws + pl.ids);
+    float* p = reinterpret_cast<float*>(ws + pl.p);
+    float* lp = backward ? nullptr : reinterpret_cast<float*>(ws + pl.lp);
+    teacher_kernel<<<(unsigned)((rows + kTeacherWarps - 1) / kTeacherWarps), kTeacherWarps * 32, 0,
+                     c.stream>>>(c.ids + t0 * c.K, c.logits + t0 * c.K, rows, (int)c.K, (int)c.V,
+                                 c.scale, ids, p, lp, f, ds->status);
+    const fp8rl_status st = cuda_check(cudaGetLastError(), "teacher_kernel launch");
+    if (st != FP8RL_OK) return st;
+    flags = f;
+    va->ids = ids;
+    va->p = p;
+  }
+  RowsArgs r = {};
+  r.flags = flags;
+  r.T = rows;
+  r.V = (int)c.V;
+  r.H = (int)c.H;
+  r.rows_per_cta = (int)std::max<int64_t>(8, (rows + 4 * ds->sm_count - 1) / (4 * ds->sm_count));
+  r.hidden = reinterpret_cast<const __nv_bfloat16*>(c.hidden) + t0 * c.ldh;
+  r.ldh = c.ldh;
+  r.x = reinterpret_cast<__nv_bfloat16*>(ws + pl.x);
+  r.map = reinterpret_cast<int32_t*>(ws + pl.map);
+  r.tgt = reinterpret_cast<int32_t*>(ws + pl.tgt);
+  r.n_rows = reinterpret_cast<int32_t*>(ws + pl.n);
+  if (backward) {
+    r.lse = c.lse + t0;
+    r.grad = c.grad + t0;
+    r.coef = coef;
+    r.lse_c = reinterpret_cast<float*>(ws + pl.lse);
+    r.gcoef_c = reinterpret_cast<float*>(ws + pl.gcoef);
+    r.grad_hidden = reinterpret_cast<__nv_bfloat16*>(c.grad_hidden);
+  } else {
+    r.out0 = c.out + t0;
+    r.out1 = c.lse_out + t0;
+  }
+  r.status = ds->status;
+  rows_kernel<<<(unsigned)((rows + r.rows_per_cta - 1) / r.rows_per_cta), kRowThreads, 0, c.stream>>>(r);
+  va->x = r.x;
+  va->w = reinterpret_cast<const __nv_bfloat16*>(c.weight);
+  va->ldw = c.ldw;
+  va->H = (int)c.H;
+  va->V = (int)c.V;
+  va->rows_cap = (int)rows;
+  va->rows_pad = (int)pl.rows_pad;
+  va->n_rows = r.n_rows;
+  va->map = r.map;
+  va->scale = c.scale;
+  va->tgt = r.tgt;
+  va->K = (int)c.K;
+  va->status = ds->status;
+  return cuda_check(cudaGetLastError(), "rows_kernel launch");
+}
+
+fp8rl_status run_forward(const Call& c) {
+  fp8rl_status st = check_call(c, false);
+  if (st != FP8RL_OK) return st;
+  if (c.T == 0) return ok();
+  DeviceState* ds = nullptr;
+  if ((st = device_state(&ds)) != FP8RL_OK) return st;
+  const Plan pl = make_plan(c.T, c.H, c.V, c.K, false);
+  for (int64_t t0 = 0; t0 < c.T; t0 += pl.rows) {
+    const int64_t rows = std::min(pl.rows, c.T - t0);
+    VocabArgs va = {};
+    if ((st = pack_rows(c, pl, ds, t0, rows, false, 0.0f, &va)) != FP8RL_OK) return st;
+    va.part = reinterpret_cast<float2*>(c.ws + pl.part);
+    va.zt = reinterpret_cast<float*>(c.ws + pl.zt);
+    if ((st = vocab_forward(va, ds, c.stream)) != FP8RL_OK) return st;
+    CombineArgs b = {};
+    b.n_rows = va.n_rows;
+    b.map = va.map;
+    b.part = va.part;
+    b.parts = (int)((c.V + kVocabPart - 1) / kVocabPart);
+    b.rows_pad = va.rows_pad;
+    b.K = va.K;
+    b.zt = va.zt;
+    b.p = va.p;
+    b.lp = reinterpret_cast<const float*>(c.ws + pl.lp);
+    b.scale = c.scale;
+    b.out = c.out + t0;
+    b.lse = c.lse_out + t0;
+    combine_kernel<<<(unsigned)((rows + 31) / 32), 1024, 0, c.stream>>>(b);
+    if ((st = cuda_check(cudaGetLastError(), "combine_kernel launch")) != FP8RL_OK) return st;
+  }
+  return ok();
+}
+
+fp8rl_status run_backward(const Call& c, float coef) {
+  fp8rl_status st = check_call(c, true);
+  if (st != FP8RL_OK) return st;
+  DeviceState* ds = nullptr;
+  if ((st = device_state(&ds)) != FP8RL_OK) return st;
+  if (c.T == 0) {
+    if (c.grad_weight)
+      st = cuda_check(cudaMemsetAsync(c.grad_weight, 0, (size_t)c.V * c.H * 2, c.stream),
+                      "cudaMemsetAsync(grad_weight)");
+    return st == FP8RL_OK ? ok() : st;
+  }
+  const Plan pl = make_plan(c.T, c.H, c.V, c.K, true);
+  VocabArgs va = {};
+  if ((st = pack_rows(c, pl, ds, 0, c.T, true, coef, &va)) != FP8RL_OK) return st;
+  va.lse = reinterpret_cast<const float*>(c.ws + pl.lse);
+  va.gcoef = reinterpret_cast<const float*>(c.ws + pl.gcoef);
+  va.g = reinterpret_cast<__nv_bfloat16*>(c.ws + pl.g);
+  va.ldg = pl.vc;
+  va.dx = c.grad_hidden ? reinterpret_cast<float*>(c.ws + pl.dx) : nullptr;
+  va.dw = reinterpret_cast<__nv_bfloat16*>(c.grad_weight);
+  for (int64_t v0 = 0; v0 < c.V; v0 += pl.vc) {
+    const int vc = (int)std::min(pl.vc, c.V - v0);
+    if ((st = vocab_backward_piece(va, (int)v0, vc, v0 == 0, ds, c.stream)) != FP8RL_OK) return st;
+  }
+  if (c.grad_hidden) {
+    const int64_t vecs = c.T * (c.H / 8);
+    scatter_kernel<<<(unsigned)std::min<int64_t>((vecs + 255) / 256, 8 * ds->sm_count), 256, 0,
+                     c.stream>>>(va.dx, va.n_rows, va.map, (int)c.H,
+                                 reinterpret_cast<__nv_bfloat16*>(c.grad_hidden));
+    if ((st = cuda_check(cudaGetLastError(), "scatter_kernel launch")) != FP8RL_OK) return st;
+  }
+  return ok();
+}
+
+}  // namespace
+}  // namespace fp8rl
+
+using namespace fp8rl;
+
+extern "C" size_t fp8rl_vocab_workspace_bytes(int64_t tokens, int64_t hidden_dim, int64_t vocab,
+                                              int32_t top_k, int32_t backward) {
+  if (!shape_ok(tokens, hidden_dim, vocab, top_k)) return 0;
+  return make_plan(tokens, hidden_dim, vocab, top_k, backward != 0).bytes;
+}
+
+extern "C" fp8rl_status fp8rl_token_logprobs(const void* hidden, int64_t ldh, const void* weight,
+                                             int64_t ldw, const int32_t* targets, int64_t tokens,
+                                             int64_t hidden_dim, int64_t vocab, float logit_scale,
+                                             float* logp, float* lse, void* workspace,
+                                             size_t workspace_bytes, cudaStream_t stream) {
+  Call c = {};
+  c.hidden = hidden; c.ldh = ldh; c.weight = weight; c.ldw = ldw;
+  c.targets = targets;
+  c.T = tokens; c.H = hidden_dim; c.V = vocab;
+  c.scale = logit_scale;
+  c.out = logp; c.lse_out = lse;
+  c.ws = static_cast<char*>(workspace); c.ws_bytes = workspace_bytes; c.stream = stream;
+  return run_forward(c);
+}
+
+extern "C" fp8rl_status fp8rl_token_logprobs_backward(
+    const void* hidden, int64_t ldh, const void* weight, int64_t ldw, const int32_t* targets,
+    const float* lse, const float* grad_logp, int64_t tokens, int64_t hidden_dim, int64_t vocab,
+    float logit_scale, void* grad_hidden, void* grad_weight, void* workspace,
+    size_t workspace_bytes, cudaStream_t stream) {
+  Call c = {};
+  c.hidden = hidden; c.ldh = ldh; c.weight = weight; c.ldw = ldw;
+  c.targets = targets; c.lse = lse; c.grad = grad_logp;
+  c.T = tokens; c.H = hidden_dim; c.V = vocab;
+  c.scale = logit_scale;
+  c.grad_hidden = grad_hidden; c.grad_weight = grad_weight;
+  c.ws = static_cast<char*>(workspace); c.ws_bytes = workspace_bytes; c.stream = stream;
+  return run_backward(c, -logit_scale);
+}
+
+extern "C" fp8rl_status fp8rl_distill_topk(const void* hidden, int64_t ldh, const void* weight,
+                                           int64_t ldw, const int32_t* teacher_ids,
+                                           const float* teacher_logits, int32_t top_k,
+                                           int64_t tokens, int64_t hidden_dim, int64_t vocab,
+                                           float logit_scale, float* loss, float* lse,
+                                           void* workspace, size_t workspace_bytes,
+                                           cudaStream_t stream) {
+  if (top_k < 1 || top_k > kMaxTopK)
+    return fail(FP8RL_ERR_UNSUPPORTED_SHAPE, "need 1 <= top_k <= %d (got %d)", kMaxTopK, top_k);
+  Call c = {};
+  c.hidden = hidden; c.ldh = ldh; c.weight = weight; c.ldw = ldw;
+  c.ids = teacher_ids; c.logits = teacher_logits; c.K = top_k;
+  c.T = tokens; c.H = hidden_dim; c.V = vocab;
+  c.scale = logit_scale;
+  c.out = loss; c.lse_out = lse;
+  c.ws = static_cast<char*>(workspace); c.ws_bytes = workspace_bytes; c.stream = stream;
+  return run_forward(c);
+}
+
+extern "C" fp8rl_status fp8rl_distill_topk_backward(
+    const void* hidden, int64_t ldh, const void* weight, int64_t ldw, const int32_t* teacher_ids,
+    const float* teacher_logits, int32_t top_k, const float* lse, const float* grad_loss,
+    int64_t tokens, int64_t hidden_dim, int64_t vocab, float logit_scale, void* grad_hidden,
+    void* grad_weight, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (top_k < 1 || top_k > kMaxTopK)
+    return fail(FP8RL_ERR_UNSUPPORTED_SHAPE, "need 1 <= top_k <= %d (got %d)", kMaxTopK, top_k);
+  Call c = {};
+  c.hidden = hidden; c.ldh = ldh; c.weight = weight; c.ldw = ldw;
+  c.ids = teacher_ids; c.logits = teacher_logits; c.K = top_k;
+  c.lse = lse; c.grad = grad_loss;
+  c.T = tokens; c.H = hidden_dim; c.V = vocab;
+  c.scale = logit_scale;
+  c.grad_hidden = grad_hidden; c.grad_weight = grad_weight;
+  c.ws = static_cast<char*>(workspace); c.ws_bytes = workspace_bytes; c.stream = stream;
+  return run_backward(c, logit_scale);
+}

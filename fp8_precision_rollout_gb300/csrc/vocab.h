@@ -1,0 +1,60 @@
+// vocab.h -- what the vocabulary operators' two translation units share:
+// vocab.cu (argument checks, row compaction, reductions) and vocab_gemm.cu
+// (the matrix products over the vocabulary and their epilogues).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "internal.h"
+
+namespace fp8rl {
+
+// Columns of the vocabulary that one softmax partial covers.
+constexpr int kVocabPart = 64;
+// Row counts are padded to this in the workspace.
+constexpr int kVocabRowPad = 256;
+
+// One call's operands on the compacted rows: row c of `x` is the hidden state
+// of token map[c]; rows that carry no target are not in it.  n_rows (device)
+// is their number, at most rows_cap.
+struct VocabArgs {
+  const __nv_bfloat16* x;   // [rows_pad, H]
+  const __nv_bfloat16* w;   // [V, H], row stride ldw
+  int64_t ldw;
+  int H, V;
+  int rows_cap, rows_pad;
+  const int32_t* n_rows;
+  const int32_t* map;       // [rows_pad] token of each compact row
+  float scale;              // logits = scale * x w^T
+  // sparse target distribution: K = 0, one target tgt[c] of probability 1;
+  // K > 0, entries ids/p[map[c] * K + j], ids ascending, absent ones INT_MAX
+  const int32_t* tgt;
+  const int32_t* ids;
+  const float* p;
+  int K;
+  // forward: per (column part, row) the maximum of x w^T and the sum of
+  // exp(scale * (x w^T - maximum)) less 1, the maximum's own term ((-inf, -1)
+  // for nothing); the entries' x w^T ([row] or [row, K])
+  float2* part;             // [ceil(V / kVocabPart), rows_pad]
+  float* zt;
+  // backward: log-sum-exp and signed, scaled upstream gradient of each row;
+  // G = gcoef * (softmax - target distribution) of columns [v0, v0 + vc)
+  const float* lse;
+  const float* gcoef;
+  __nv_bfloat16* g;         // [rows_pad, ldg]
+  int64_t ldg;
+  float* dx;                // [rows_pad, H] FP32 sums over the vocabulary pieces
+  __nv_bfloat16* dw;        // [V, H] or null
+  uint32_t* status;
+};
+
+// Softmax partials and target logits of every row over the whole vocabulary.
+fp8rl_status vocab_forward(const VocabArgs& a, const DeviceState* ds, cudaStream_t stream);
+// One piece [v0, v0 + vc) of the vocabulary: G, dx += G W (stored when
+// `first`), dw rows [v0, v0 + vc) = G^T x.  dx and/or dw may be null.
+fp8rl_status vocab_backward_piece(const VocabArgs& a, int v0, int vc, bool first,
+                                  const DeviceState* ds, cudaStream_t stream);
+
+}  // namespace fp8rl

@@ -10,7 +10,10 @@
  *   - a blockwise-scaled FP8 W8A8 GEMM with FP32 accumulation and BF16
  *     output, plus a grouped variant for MoE experts,
  *   - FP8 E4M3 KV-cache quantization with per-head scales,
- *   - token-level truncated importance-sampling (TIS) weights.
+ *   - token-level truncated importance-sampling (TIS) weights,
+ *   - the token log-probabilities they are made of, from a model's last hidden
+ *     states and vocabulary weights, with gradients, and distillation from a
+ *     teacher's top entries over the same head.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -378,10 +381,109 @@ fp8rl_status fp8rl_is_weights_stats_loss(const float* logp_train, const float* l
                                          float c_hi, float c_lo, int32_t mode, float* w,
                                          double* stats, cudaStream_t stream);
 
+/* Token log-probabilities under a language-model head, without the logits.
+ * Section 3.4.3: the importance weight is exp(logp_train - logp_rollout); this
+ * call computes such a log-probability from the model's last hidden states.
+ * With z_tv = logit_scale * <hidden_t, weight_v> (BF16 products summed in
+ * FP32 or better):
+ *   lse[t]  = log sum_v exp z_tv           (natural log, v < vocab)
+ *   logp[t] = z_t,targets[t] - lse[t]
+ * A token whose target is negative is left out: both outputs are 0, and what
+ * its hidden state holds is not used.  A target >= vocab is treated alike and
+ * sets the bit that fp8rl_device_status reports.  The [tokens, vocab] logits
+ * are never stored: softmax partials of 128-column parts are, for at most
+ * about 128 MB of them at a time.
+ *   hidden   BF16 [tokens, hidden_dim], row stride ldh (>= hidden_dim,
+ *            multiple of 8), 16-byte aligned; NULL only when tokens == 0
+ *   weight   BF16 [vocab, hidden_dim], row stride ldw (as ldh), 16-byte aligned
+ *   targets  int32 [tokens]
+ *   logit_scale  finite, > 0 (1 / temperature)
+ *   logp, lse  FP32 [tokens], overwritten
+ *   workspace  DEVICE memory owned by the caller, 256-byte aligned, at least
+ *            fp8rl_vocab_workspace_bytes(tokens, hidden_dim, vocab, 0, 0)
+ *            bytes; its contents need not be set and mean nothing afterwards;
+ *            calls that overlap on the GPU need separate workspaces
+ * Requires hidden_dim a multiple of 8 in [8, 2^20], 0 <= tokens <= 2^30,
+ * 1 <= vocab <= 2^30; tokens = 0 is a no-op.  Sums are FP32, in an order that
+ * depends on the sizes alone: results repeat bit for bit. */
+fp8rl_status fp8rl_token_logprobs(const void* hidden, int64_t ldh, const void* weight, int64_t ldw,
+                                  const int32_t* targets, int64_t tokens, int64_t hidden_dim,
+                                  int64_t vocab, float logit_scale, float* logp, float* lse,
+                                  void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Gradient of sum_t grad_logp[t] * logp[t] (fp8rl_token_logprobs) with
+ * respect to hidden and weight.  With q_tv = exp(z_tv - lse[t]):
+ *   G_tv        = grad_logp[t] * logit_scale * ([v == targets[t]] - q_tv)
+ *   grad_hidden = G weight        grad_weight = G^T hidden
+ * The logits are computed again, piece of the vocabulary by piece; a piece's
+ * G is held in BF16 (one rounding, 2^-9 relative; at most about 192 MB, or 256
+ * columns), the sums over it are FP32, and each gradient is rounded to BF16
+ * once.  Tokens left out get zero rows of grad_hidden and add nothing.
+ *   lse          FP32 [tokens] as fp8rl_token_logprobs wrote it
+ *   grad_logp    FP32 [tokens]
+ *   grad_hidden  BF16 [tokens, hidden_dim] dense, 16-byte aligned, or NULL
+ *   grad_weight  BF16 [vocab, hidden_dim] dense, 16-byte aligned, or NULL
+ *                (at least one of the two); overwritten, not accumulated into
+ *   workspace    at least fp8rl_vocab_workspace_bytes(tokens, hidden_dim,
+ *                vocab, 0, 1) bytes; otherwise as above
+ * Other arguments and requirements as in fp8rl_token_logprobs; tokens = 0
+ * sets grad_weight to zero. */
+fp8rl_status fp8rl_token_logprobs_backward(const void* hidden, int64_t ldh, const void* weight,
+                                           int64_t ldw, const int32_t* targets, const float* lse,
+                                           const float* grad_logp, int64_t tokens,
+                                           int64_t hidden_dim, int64_t vocab, float logit_scale,
+                                           void* grad_hidden, void* grad_weight, void* workspace,
+                                           size_t workspace_bytes, cudaStream_t stream);
+
+/* Distillation from a teacher's top entries over the same head (an
+ * engineering addition; the pages have no counterpart).  Token t's entries
+ * are teacher_ids[t][k], teacher_logits[t][k] (logits or log-probabilities,
+ * in any order, k < top_k); one is present if 0 <= id < vocab and its logit is
+ * not -inf (an id >= vocab also sets the bit fp8rl_device_status reports).
+ * With p the softmax of logit_scale * teacher_logits over the present
+ * entries and log q_v = z_tv - lse[t] the student's over the whole vocabulary:
+ *   loss[t] = sum_k p_k (log p_k - log q_id_k)        (terms with p_k = 0 are 0)
+ * the forward KL divergence from the teacher's top entries.  Repeated ids
+ * count each.  A token without present entries is left out (loss and lse 0).
+ *   teacher_ids     int32 [tokens, top_k] dense
+ *   teacher_logits  FP32 [tokens, top_k] dense
+ *   top_k           1 .. 256
+ *   loss, lse       FP32 [tokens], overwritten
+ *   workspace       fp8rl_vocab_workspace_bytes(tokens, hidden_dim, vocab,
+ *                   top_k, 0)
+ * Other arguments, requirements and errors as in fp8rl_token_logprobs. */
+fp8rl_status fp8rl_distill_topk(const void* hidden, int64_t ldh, const void* weight, int64_t ldw,
+                                const int32_t* teacher_ids, const float* teacher_logits,
+                                int32_t top_k, int64_t tokens, int64_t hidden_dim, int64_t vocab,
+                                float logit_scale, float* loss, float* lse, void* workspace,
+                                size_t workspace_bytes, cudaStream_t stream);
+
+/* Gradient of sum_t grad_loss[t] * loss[t] (fp8rl_distill_topk) with respect
+ * to hidden and weight: G_tv = grad_loss[t] * logit_scale * (q_tv - sum of the
+ * p_k with id_k == v), then as fp8rl_token_logprobs_backward.  The teacher's
+ * entries take no gradient.
+ *   lse        FP32 [tokens] as fp8rl_distill_topk wrote it
+ *   grad_loss  FP32 [tokens]
+ *   workspace  fp8rl_vocab_workspace_bytes(tokens, hidden_dim, vocab, top_k, 1) */
+fp8rl_status fp8rl_distill_topk_backward(const void* hidden, int64_t ldh, const void* weight,
+                                         int64_t ldw, const int32_t* teacher_ids,
+                                         const float* teacher_logits, int32_t top_k,
+                                         const float* lse, const float* grad_loss, int64_t tokens,
+                                         int64_t hidden_dim, int64_t vocab, float logit_scale,
+                                         void* grad_hidden, void* grad_weight, void* workspace,
+                                         size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes of the four calls above: top_k = 0 for the log-probability
+ * pair, backward != 0 for the gradients.  0 for sizes they do not support.
+ * Host-only: no device is touched. */
+size_t fp8rl_vocab_workspace_bytes(int64_t tokens, int64_t hidden_dim, int64_t vocab,
+                                   int32_t top_k, int32_t backward);
+
 /* Synchronizes the device and returns FP8RL_ERR_TIMEOUT if any kernel since
  * the last clear hit a device-side wait limit, FP8RL_ERR_INVALID_ARG if a
  * kernel met an out-of-range device-side index (fp8rl_quantize_act_gather,
- * fp8rl_decode_attention_fp8kv),
+ * fp8rl_decode_attention_fp8kv, the token log-probability and distillation
+ * calls),
  * FP8RL_OK otherwise; clears the word when clear != 0.  device = CUDA
  * ordinal. */
 fp8rl_status fp8rl_device_status(int32_t device, int32_t clear);

@@ -565,3 +565,90 @@ def tis_weights(logp_train, logp_rollout, mask=None, c_hi: float = 2.0, c_lo: fl
     if mask is not None:
         w = np.where(np.asarray(mask) == 0, np.float32(0), w)
     return w.astype(np.float32)
+
+
+# ------------------------------------------------- the vocabulary operators --
+
+def _f64(x) -> np.ndarray:
+    return (x.detach().cpu().double().numpy() if hasattr(x, "detach") else np.asarray(x, np.float64))
+
+
+def head_softmax(hidden, weight, scale: float = 1.0):
+    """(z, mag, lse) in float64: z = scale * hidden @ weight^T [T, V], the sums
+    of magnitudes behind each z, and each row's log-sum-exp."""
+    h, w = _f64(hidden), _f64(weight)
+    s = float(np.float32(scale))
+    z = s * (h @ w.T)
+    mag = s * (np.abs(h) @ np.abs(w).T)
+    top = z.max(axis=1, keepdims=True)
+    lse = np.log(np.exp(z - top).sum(axis=1)) + top[:, 0]
+    return z, mag, lse
+
+
+def one_hot_targets(targets, vocab: int):
+    """Target distribution [T, V] and kept tokens [T] of token log-probabilities:
+    a target outside [0, vocab) leaves its token out."""
+    t = np.asarray(targets)
+    kept = (t >= 0) & (t < vocab)
+    d = np.zeros((t.size, vocab))
+    d[np.nonzero(kept)[0], t[kept]] = 1.0
+    return d, kept
+
+
+def teacher_entries(ids, logits, vocab: int, scale: float = 1.0):
+    """(p, log p, present) [T, K] and kept tokens [T] of a teacher's entries:
+    softmax of scale * logits over the entries with 0 <= id < vocab whose
+    scaled logit is not -inf; p is 0 and log p is 0 elsewhere."""
+    ids = np.asarray(ids)
+    u = np.asarray(logits, np.float64) * float(np.float32(scale))
+    there = (ids >= 0) & (ids < vocab) & ~np.isneginf(u)
+    kept = there.any(axis=1)
+    p, lp = np.zeros(u.shape), np.zeros(u.shape)
+    for t in np.nonzero(kept)[0]:
+        x = u[t, there[t]]
+        x = x - x.max()
+        l = x - np.log(np.exp(x).sum())
+        lp[t, there[t]] = l
+        p[t, there[t]] = np.exp(l)
+    return p, lp, there, kept
+
+
+def token_logprobs(hidden, weight, targets, scale: float = 1.0):
+    """(logp, lse) float64 [T] of section 3.4.3's token log-probabilities
+    (0, 0 for a token that is left out)."""
+    z, _, lse = head_softmax(hidden, weight, scale)
+    _, kept = one_hot_targets(targets, z.shape[1])
+    t = np.where(kept, np.asarray(targets), 0)
+    logp = z[np.arange(t.size), t] - lse
+    return np.where(kept, logp, 0.0), np.where(kept, lse, 0.0)
+
+
+def distill_topk(hidden, weight, ids, logits, scale: float = 1.0):
+    """(loss, lse) float64 [T]: sum_k p_k (log p_k - log q_id_k) against the
+    student's softmax over the whole vocabulary."""
+    z, _, lse = head_softmax(hidden, weight, scale)
+    p, lp, there, kept = teacher_entries(ids, logits, z.shape[1], scale)
+    safe = np.where(there, np.asarray(ids), 0)
+    log_q = np.take_along_axis(z, safe, axis=1) - lse[:, None]
+    loss = np.where(there & (p > 0), p * (lp - log_q), 0.0).sum(axis=1)
+    return np.where(kept, loss, 0.0), np.where(kept, lse, 0.0)
+
+
+def head_gradients(hidden, weight, dist, kept, grad, sign: float, scale: float = 1.0):
+    """(grad_hidden, grad_weight, G, q) float64 for G = sign * grad * scale *
+    (q - dist) on the kept tokens: sign -1 and one_hot_targets for the token
+    log-probabilities, +1 and the teacher's distribution for distillation."""
+    z, _, lse = head_softmax(hidden, weight, scale)
+    q = np.exp(z - lse[:, None])
+    g = np.where(kept, np.asarray(grad, np.float64), 0.0) * float(np.float32(scale)) * sign
+    G = np.where(kept[:, None], g[:, None] * (q - dist), 0.0)
+    h = np.where(kept[:, None], _f64(hidden), 0.0)
+    return G @ _f64(weight), G.T @ h, G, q
+
+
+def dense_teacher(ids, p, there, vocab: int) -> np.ndarray:
+    """The teacher's entries as a distribution [T, vocab] (repeated ids add up)."""
+    d = np.zeros((np.asarray(ids).shape[0], vocab))
+    for t, k in zip(*np.nonzero(there)):
+        d[t, np.asarray(ids)[t, k]] += p[t, k]
+    return d
