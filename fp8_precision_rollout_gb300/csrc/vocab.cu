@@ -275,17 +275,24 @@ __global__ void __launch_bounds__(1024) combine_kernel(const CombineArgs a) {
   }
 }
 
-// dX of the compact rows (FP32) -> grad_hidden rows of their tokens.
+// dX of the packed rows (FP32, the slices' sums added in order) -> grad_hidden
+// rows of their tokens.
 __global__ void __launch_bounds__(256)
     scatter_kernel(const float* dx, const int32_t* n_rows, const int32_t* map, int H,
-                   __nv_bfloat16* grad_hidden) {
+                   int slices, int64_t slice_stride, __nv_bfloat16* grad_hidden) {
   const int vecs = H / 8;
   const int64_t total = (int64_t)*n_rows * vecs;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t c = i / vecs;
     const int v = (int)(i - c * vecs);
     const float4* src = reinterpret_cast<const float4*>(dx + c * H + v * 8);
-    const float4 x = src[0], y = src[1];
+    float4 x = src[0], y = src[1];
+    for (int k = 1; k < slices; ++k) {
+      src = reinterpret_cast<const float4*>(dx + k * slice_stride + c * H + v * 8);
+      const float4 x2 = src[0], y2 = src[1];
+      x.x += x2.x; x.y += x2.y; x.z += x2.z; x.w += x2.w;
+      y.x += y2.x; y.y += y2.y; y.z += y2.z; y.w += y2.w;
+    }
     __nv_bfloat162 b[4] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w),
                            __floats2bfloat162_rn(y.x, y.y), __floats2bfloat162_rn(y.z, y.w)};
     *reinterpret_cast<uint4*>(grad_hidden + (int64_t)map[c] * H + v * 8) =
@@ -300,7 +307,8 @@ struct Plan {
   int64_t rows = 0;        // tokens handled at once (forward: a piece of them)
   int64_t rows_pad = 0;
   int64_t vc = 0;          // backward: vocabulary columns of a piece
-  size_t x, map, tgt, n, part, zt, lse, gcoef, g, dx, flags, ids, p, lp, bytes;
+  int slices = 1;          // backward: separate sums of dX
+  size_t x, map, tgt, n, part, zt, lse, gcoef, g0, g1, dx, flags, ids, p, lp, bytes;
 };
 
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
@@ -309,17 +317,17 @@ int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 // workspace grows with neither tokens x vocab nor tokens beyond a piece.
 // Backward: the vocabulary goes in pieces whose G fits kGradBytes.
 constexpr int64_t kPartBytes = 128ll << 20;
-constexpr int64_t kGradBytes = 192ll << 20;
+constexpr int64_t kGradBytes = 192ll << 20;   // each of two buffers
 
 Plan make_plan(int64_t T, int64_t H, int64_t V, int64_t K, bool backward) {
   Plan pl;
   const int64_t parts = (V + kVocabPart - 1) / kVocabPart;
   pl.rows = T;
   if (!backward) {
-    const int64_t most = std::max<int64_t>(2048, kPartBytes / (parts * 8) / kVocabRowPad * kVocabRowPad);
+    const int64_t most = std::max<int64_t>(2048, kPartBytes / (parts * 8) / kVocabPad * kVocabPad);
     pl.rows = std::min(T, most);
   }
-  pl.rows_pad = round_up(std::max<int64_t>(pl.rows, 1), kVocabRowPad);
+  pl.rows_pad = round_up(std::max<int64_t>(pl.rows, 1), kVocabPad);
   size_t at = 0;
   const auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -334,12 +342,15 @@ Plan make_plan(int64_t T, int64_t H, int64_t V, int64_t K, bool backward) {
     pl.part = take((size_t)pl.rows_pad * parts * 8);
     pl.zt = take((size_t)pl.rows_pad * std::max<int64_t>(K, 1) * 4);
   } else {
-    pl.vc = std::max<int64_t>(256, kGradBytes / (pl.rows_pad * 2) / 256 * 256);
-    pl.vc = std::min(pl.vc, round_up(V, 256));
+    const int64_t most = std::max<int64_t>(kVocabPad, kGradBytes / (pl.rows_pad * 2) / kVocabPad * kVocabPad);
+    const int64_t pieces = (V + most - 1) / most;
+    pl.vc = round_up((V + pieces - 1) / pieces, kVocabPad);
+    pl.slices = vocab_dx_slices(pl.rows_pad, H, std::min(pl.vc, V));
     pl.lse = take((size_t)pl.rows_pad * 4);
     pl.gcoef = take((size_t)pl.rows_pad * 4);
-    pl.g = take((size_t)pl.rows_pad * pl.vc * 2);
-    pl.dx = take((size_t)pl.rows_pad * H * 4);
+    pl.g0 = take((size_t)pl.rows_pad * pl.vc * 2);
+    pl.g1 = pieces > 1 ? take((size_t)pl.rows_pad * pl.vc * 2) : pl.g0;
+    pl.dx = take((size_t)pl.slices * pl.rows_pad * H * 4);
   }
   if (K) {
     pl.flags = take((size_t)pl.rows_pad * 4);
@@ -522,18 +533,17 @@ fp8rl_status run_backward(const Call& c, float coef) {
   if ((st = pack_rows(c, pl, ds, 0, c.T, true, coef, &va)) != FP8RL_OK) return st;
   va.lse = reinterpret_cast<const float*>(c.ws + pl.lse);
   va.gcoef = reinterpret_cast<const float*>(c.ws + pl.gcoef);
-  va.g = reinterpret_cast<__nv_bfloat16*>(c.ws + pl.g);
-  va.ldg = pl.vc;
+  va.g[0] = reinterpret_cast<__nv_bfloat16*>(c.ws + pl.g0);
+  va.g[1] = reinterpret_cast<__nv_bfloat16*>(c.ws + pl.g1);
+  va.vc = (int)pl.vc;
+  va.slices = pl.slices;
   va.dx = c.grad_hidden ? reinterpret_cast<float*>(c.ws + pl.dx) : nullptr;
   va.dw = reinterpret_cast<__nv_bfloat16*>(c.grad_weight);
-  for (int64_t v0 = 0; v0 < c.V; v0 += pl.vc) {
-    const int vc = (int)std::min(pl.vc, c.V - v0);
-    if ((st = vocab_backward_piece(va, (int)v0, vc, v0 == 0, ds, c.stream)) != FP8RL_OK) return st;
-  }
+  if ((st = vocab_backward(va, ds, c.stream)) != FP8RL_OK) return st;
   if (c.grad_hidden) {
     const int64_t vecs = c.T * (c.H / 8);
     scatter_kernel<<<(unsigned)std::min<int64_t>((vecs + 255) / 256, 8 * ds->sm_count), 256, 0,
-                     c.stream>>>(va.dx, va.n_rows, va.map, (int)c.H,
+                     c.stream>>>(va.dx, va.n_rows, va.map, (int)c.H, va.slices, (int64_t)va.rows_pad * c.H,
                                  reinterpret_cast<__nv_bfloat16*>(c.grad_hidden));
     if ((st = cuda_check(cudaGetLastError(), "scatter_kernel launch")) != FP8RL_OK) return st;
   }

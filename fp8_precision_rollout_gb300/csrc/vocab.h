@@ -1,6 +1,6 @@
 // vocab.h -- what the vocabulary operators' two translation units share:
-// vocab.cu (argument checks, row compaction, reductions) and vocab_gemm.cu
-// (the matrix products over the vocabulary and their epilogues).
+// vocab.cu (argument checks, row packing, reductions) and vocab_gemm.cu (the
+// matrix products over the vocabulary and their epilogues).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -12,13 +12,14 @@
 namespace fp8rl {
 
 // Columns of the vocabulary that one softmax partial covers.
-constexpr int kVocabPart = 64;
-// Row counts are padded to this in the workspace.
-constexpr int kVocabRowPad = 256;
+constexpr int kVocabPart = 128;
+// Row counts, and pieces of the vocabulary, are padded to this in the
+// workspace: the tile's rows and columns.
+constexpr int kVocabPad = 256;
 
-// One call's operands on the compacted rows: row c of `x` is the hidden state
-// of token map[c]; rows that carry no target are not in it.  n_rows (device)
-// is their number, at most rows_cap.
+// One call's operands on the packed rows: row c of `x` is the hidden state of
+// token map[c]; tokens without a target are not in it.  n_rows (device) is
+// their number, at most rows_cap.
 struct VocabArgs {
   const __nv_bfloat16* x;   // [rows_pad, H]
   const __nv_bfloat16* w;   // [V, H], row stride ldw
@@ -26,7 +27,7 @@ struct VocabArgs {
   int H, V;
   int rows_cap, rows_pad;
   const int32_t* n_rows;
-  const int32_t* map;       // [rows_pad] token of each compact row
+  const int32_t* map;       // [rows_pad] token of each packed row
   float scale;              // logits = scale * x w^T
   // sparse target distribution: K = 0, one target tgt[c] of probability 1;
   // K > 0, entries ids/p[map[c] * K + j], ids ascending, absent ones INT_MAX
@@ -40,21 +41,22 @@ struct VocabArgs {
   float2* part;             // [ceil(V / kVocabPart), rows_pad]
   float* zt;
   // backward: log-sum-exp and signed, scaled upstream gradient of each row;
-  // G = gcoef * (softmax - target distribution) of columns [v0, v0 + vc)
+  // G = gcoef * (softmax - target distribution)
   const float* lse;
   const float* gcoef;
-  __nv_bfloat16* g;         // [rows_pad, ldg]
-  int64_t ldg;
-  float* dx;                // [rows_pad, H] FP32 sums over the vocabulary pieces
-  __nv_bfloat16* dw;        // [V, H] or null
+  __nv_bfloat16* g[2];      // [rows_pad, vc] each: alternating pieces of G
+  int vc;                   // columns of a piece, a multiple of kVocabPad
+  int slices;               // dX: sums over this many parts of a piece
+  float* dx;                // [slices, rows_pad, H] FP32, or null
+  __nv_bfloat16* dw;        // [V, H], or null
   uint32_t* status;
 };
 
 // Softmax partials and target logits of every row over the whole vocabulary.
 fp8rl_status vocab_forward(const VocabArgs& a, const DeviceState* ds, cudaStream_t stream);
-// One piece [v0, v0 + vc) of the vocabulary: G, dx += G W (stored when
-// `first`), dw rows [v0, v0 + vc) = G^T x.  dx and/or dw may be null.
-fp8rl_status vocab_backward_piece(const VocabArgs& a, int v0, int vc, bool first,
-                                  const DeviceState* ds, cudaStream_t stream);
+// G, dx (per slice) and dw over the whole vocabulary, piece by piece.
+fp8rl_status vocab_backward(const VocabArgs& a, const DeviceState* ds, cudaStream_t stream);
+// Slices that give the dX product of `rows` x H enough tiles to fill the GPU.
+int vocab_dx_slices(int64_t rows, int64_t H, int64_t vc);
 
 }  // namespace fp8rl

@@ -1,156 +1,713 @@
-// vocab_gemm.cu -- the matrix products of the vocabulary operators.
+// vocab_gemm.cu -- the matrix products of the vocabulary operators, on tcgen05
+// tensor cores.
 //
-//   forward   A = X W^T, reduced in the epilogue to softmax partials;
-//   G         the same product, turned into gcoef * (softmax - targets), BF16;
-//   dX        G W, FP32 sums over the vocabulary pieces;
-//   dW        G^T X.
+//   stats   Z = X W^T, reduced in the epilogue to softmax partials and the
+//           targets' logits; Z itself never leaves the SM;
+//   grad    the same product, turned into G = gcoef * (softmax - targets), BF16;
+//   dX      G W, FP32, one sum per slice of the vocabulary, added over pieces;
+//   dW      G^T X, BF16.
 //
-// Plain tiles: 64 x 64 outputs per CTA, 256 threads, 4 x 4 FP32 accumulators
-// each, operands staged through shared memory 16 deep.
+// One tile shape for all of them: 256 x 256 outputs per CTA pair
+// (cta_group::2, M = 256, N = 256), 64 deep steps.  Each CTA of the pair loads
+// its 128 rows of A and 128 of B's 256 (32 KB a step, half of what a CTA with
+// a tile of its own would load for the same products) and holds its 128 x 256
+// FP32 results in tensor memory, twice (all 512 columns), so that the tensor
+// cores fill one buffer while eight epilogue warps empty the other.
+//   warp 0     TMA producer (lane 0): both CTAs' loads count on the even
+//              CTA's barrier;
+//   warp 1     MMA issuer (lane 0 of the even CTA), commits to both CTAs;
+//   warps 2-9  epilogue: warp w reads TMEM lanes 32*(w%4).. and column half
+//              (w-2)/4.
+// Operands are K-major where the summed index is contiguous in memory (X and W
+// in Z; G in dX) and MN-major where it is the row (W in dX; G and X in dW):
+// TMA boxes of 64 elements x 64 rows, and the transposed-operand bits of the
+// instruction descriptor.  No operand is ever transposed in memory.
+//
+// Persistent, one pair of CTAs per two SMs.  The number of packed rows is known
+// on the device only; every role derives the same sequence of jobs from it.
+// Backward launches hold three kinds at once: dX and dW of one piece of the
+// vocabulary and G of the next, so that a launch has one tail, not three.
+// Every wait is bounded (1 s); see mbar_wait.
 #include <algorithm>
+#include <mutex>
 
+#include "sm100_ptx.cuh"
 #include "vocab.h"
 
 namespace fp8rl {
 namespace {
 
-constexpr int kT = 64, kD = 16;
-constexpr float kLog2e = 1.4426950408889634f;
-enum { kStats = 0, kGrad = 1, kDx = 2, kDw = 3 };
+using namespace ptx;
 
-struct Operand {
-  const __nv_bfloat16* p;
-  int64_t ld_mn, ld_k;   // element strides
+constexpr int kThreads = 320;
+constexpr int kEpiWarps = 8;
+constexpr int kTile = 256;             // rows and columns of a pair's tile
+constexpr int kBK = 64;
+constexpr int kOperand = 128 * kBK * 2;          // one operand's share of a CTA: 16 KB
+constexpr int kStageBytes = 2 * kOperand;
+constexpr int kBoxBytes = 4096;                  // output boxes: 32 rows x 128 bytes
+constexpr int kStageOutBytes = 2 * kBoxBytes;    // per epilogue warp
+constexpr int kMaxStages = 6;
+constexpr int kBand = 16;                        // row tiles per raster band
+constexpr float kLog2e = 1.4426950408889634f;
+// The tensor cores' FP32 sums of stats are cut into runs of this many steps,
+// added up in registers (see the stats epilogue).
+constexpr int kRun = 8;
+
+enum Kind { kStats = 0, kGrad = 1, kDx = 2, kDw = 3 };
+
+// kind::f16: D = F32 (bits 4-5 = 1), A = B = BF16 (bits 7-9, 10-12 = 1),
+// MN-major A and B (bits 15, 16), N >> 3 in bits 17-22, M >> 4 in bits 24-28.
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kTile >> 3) << 17) |
+                            ((uint32_t)(kTile >> 4) << 24);
+constexpr uint32_t kMnA = 1u << 15, kMnB = 1u << 16;
+
+template <bool kFwd>
+struct Cfg {
+  static constexpr int kStages = kFwd ? 6 : 5;
+  static constexpr size_t kOut = kFwd ? 0 : (size_t)kEpiWarps * kStageOutBytes;
 };
 
-template <int kEpi>
-__global__ void __launch_bounds__(256) vocab_gemm_kernel(VocabArgs a, Operand A, Operand B, int v0,
-                                                         int vc, int first) {
-  __shared__ float sA[kD][kT + 4], sB[kD][kT + 4];
-  __shared__ float red[kT][18], ties[kT][16];
-  const int n = *a.n_rows;
-  const int m0 = blockIdx.y * kT, c0 = blockIdx.x * kT;
-  const int M = kEpi == kDw ? vc : n;
-  const int N = kEpi == kStats ? a.V : (kEpi == kGrad ? vc : a.H);
-  const int K = kEpi == kDx ? vc : (kEpi == kDw ? n : a.H);
-  // G keeps zero rows up to its row padding, so every tile of it is written
-  if (m0 >= M && kEpi != kGrad) return;
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < K; k0 += kD) {
-    for (int i = tid; i < kT * kD; i += 256) {
-      const int mn = i / kD, k = i % kD;
-      sA[k][mn] = (m0 + mn < M && k0 + k < K)
-                      ? __bfloat162float(A.p[(m0 + mn) * A.ld_mn + (k0 + k) * A.ld_k]) : 0.0f;
-      sB[k][mn] = (c0 + mn < N && k0 + k < K)
-                      ? __bfloat162float(B.p[(c0 + mn) * B.ld_mn + (k0 + k) * B.ld_k]) : 0.0f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kD; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sA[k][ty * 4 + i], sB[k][tx * 4 + j], acc[i][j]);
-    __syncthreads();
+struct Tail {
+  uint64_t full[kMaxStages];
+  uint64_t empty[kMaxStages];
+  uint64_t tfull[2];
+  uint64_t tempty[2];
+  uint32_t tmem_base;
+  uint32_t abort_flag;
+};
+static_assert(sizeof(Tail) <= 1024, "");
+template <bool kFwd>
+constexpr size_t smem_bytes() {
+  return 1024 + (size_t)Cfg<kFwd>::kStages * kStageBytes + Cfg<kFwd>::kOut + 1024;
+}
+static_assert(smem_bytes<true>() <= 232448 && smem_bytes<false>() <= 232448, "shared memory budget");
+
+struct Params {
+  CUtensorMap x_k, w_k;             // stats, grad: boxes 64 x 128 rows
+  CUtensorMap g_out;                // grad: the piece written (32 x 64 boxes)
+  CUtensorMap g_k, w_mn, dx_out;    // dX
+  CUtensorMap g_mn, x_mn, dw_out;   // dW
+  VocabArgs a;
+  int v_grad;      // first vocabulary column of the grad piece
+  int n_grad;      // its column tiles (0: none)
+  int v_prod;      // first column of the piece whose products are formed
+  int vc_prod;     // its columns
+  int dx_tiles_n;  // column tiles of H when dX / dW are wanted, else 0
+  int dw_tiles_n;
+  int dx_first;    // this piece's dX is stored, not added
+};
+
+struct Job {
+  int kind;
+  int steps;      // 64-deep steps
+  int a0, b0;     // first row of A / of B (tile coordinates along M / N)
+  int k0;         // first element of the summed index
+  int slice;
+};
+
+// The job sequence of a pair: job i of pair c out of `np`.
+struct Schedule {
+  int c, np;
+  int mt;                       // row tiles
+  int slices;                   // of this piece's steps: no more than it has
+  int ndx, per, rem, early;     // dX jobs; full rounds of them; pairs with one more; see below
+  int ndw, nb;                  // dW jobs; dW + grad jobs
+  int nstats;
+};
+
+template <bool kFwd>
+__device__ __forceinline__ Schedule make_schedule(const Params& p, int n, int c, int np) {
+  Schedule s = {};
+  s.c = c;
+  s.np = np;
+  s.mt = (max(n, kFwd ? 0 : 1) + kTile - 1) / kTile;
+  if (kFwd) {
+    s.nstats = s.mt * ((p.a.V + kTile - 1) / kTile);
+    return s;
   }
-  for (int i = 0; i < 4; ++i) {
-    const int r = m0 + ty * 4 + i;
-    if (kEpi == kStats) {
-      float mx = -INFINITY;
-      for (int j = 0; j < 4; ++j)
-        if (c0 + tx * 4 + j < N) mx = fmaxf(mx, acc[i][j]);
-      for (int o = 8; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-      float s = 0.0f, cnt = 0.0f;
-      for (int j = 0; j < 4; ++j)
-        if (c0 + tx * 4 + j < N) {
-          if (acc[i][j] == mx)
-            cnt += mx == -INFINITY ? 0.0f : 1.0f;
-          else
-            s += exp2f((acc[i][j] - mx) * (a.scale * kLog2e));
-        }
-      red[ty * 4 + i][tx] = s;
-      ties[ty * 4 + i][tx] = cnt;
-      if (tx == 0) red[ty * 4 + i][16] = mx;
+  // dX jobs sum over a whole slice and are the longest: they go first, dealt
+  // round robin.  dW and grad jobs follow in order.  Where the dX jobs do not
+  // divide evenly, the pairs without the last one take the first `early`
+  // rounds of the others meanwhile, as many as fit into a dX job.
+  const int all = (p.vc_prod + kBK - 1) / kBK;
+  s.slices = min(p.a.slices, max(all, 1));
+  s.ndx = s.mt * p.dx_tiles_n * s.slices;
+  s.per = s.ndx / np;
+  s.rem = s.ndx % np;
+  s.ndw = p.dw_tiles_n ? ((p.vc_prod + kTile - 1) / kTile) * p.dw_tiles_n : 0;
+  s.nb = s.ndw + s.mt * p.n_grad;
+  const int dx_steps = (all + s.slices - 1) / s.slices;
+  const int other = s.ndw ? (n + kBK - 1) / kBK : (p.a.H + kBK - 1) / kBK;
+  s.early = s.rem ? dx_steps / max(other, 4) : 0;   // (a job's epilogue takes about 4 steps)
+  return s;
+}
+
+// Tile t of a grid of mt row tiles x any number of column tiles, in bands of
+// kBand row tiles, rows fastest: a column tile of W is used by the whole band
+// at once and the band's rows of X stay in L2.
+__device__ __forceinline__ void band_tile(int t, int mt, int tiles_n, int* m, int* nn) {
+  const int per_band = kBand * tiles_n;
+  const int band = t / per_band;
+  const int gs = min(kBand, mt - band * kBand);
+  const int local = t - band * per_band;
+  *m = band * kBand + local % gs;
+  *nn = local / gs;
+}
+
+template <bool kFwd>
+__device__ __forceinline__ bool get_job(const Params& p, const Schedule& s, int n, int i, Job* j) {
+  const int h_steps = (p.a.H + kBK - 1) / kBK;
+  if (kFwd) {
+    const int t = s.c + i * s.np;
+    if (t >= s.nstats) return false;
+    int m, nn;
+    band_tile(t, s.mt, (p.a.V + kTile - 1) / kTile, &m, &nn);
+    *j = {kStats, h_steps, m * kTile, nn * kTile, 0, 0};
+    return true;
+  }
+  const int mine = s.per + (s.c < s.rem ? 1 : 0);
+  if (i < mine) {
+    const int t = s.c + i * s.np;
+    const int nn = t % p.dx_tiles_n;
+    const int m = (t / p.dx_tiles_n) % s.mt;
+    const int slice = t / (p.dx_tiles_n * s.mt);
+    const int all = (p.vc_prod + kBK - 1) / kBK;
+    const int k0 = (int)((int64_t)all * slice / s.slices);
+    const int k1 = (int)((int64_t)all * (slice + 1) / s.slices);
+    *j = {kDx, k1 - k0, m * kTile, nn * kTile, k0 * kBK, slice};
+    return true;
+  }
+  const int k = i - mine;
+  int t;
+  if (s.c >= s.rem && k < s.early)
+    t = k * (s.np - s.rem) + (s.c - s.rem);
+  else
+    t = s.early * (s.np - s.rem) + (k - (s.c >= s.rem ? s.early : 0)) * s.np + s.c;
+  if (t >= s.nb) return false;
+  if (t < s.ndw) {
+    const int nn = t % p.dw_tiles_n, m = t / p.dw_tiles_n;
+    *j = {kDw, (max(n, 1) + kBK - 1) / kBK, m * kTile, nn * kTile, 0, 0};
+  } else {
+    int m, nn;
+    band_tile(t - s.ndw, s.mt, p.n_grad, &m, &nn);
+    *j = {kGrad, h_steps, m * kTile, nn * kTile, 0, 0};
+  }
+  return true;
+}
+
+// First of this row's entries with id >= v.
+__device__ __forceinline__ int first_entry(const int32_t* ids, int K, int v) {
+  int lo = 0, hi = K;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(ids + mid) < v) lo = mid + 1; else hi = mid;
+  }
+  return lo;
+}
+
+template <bool kFwd>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+    vocab_kernel(const __grid_constant__ Params p) {
+  constexpr int STAGES = Cfg<kFwd>::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t s_base = smem_u32(smem);
+  const uint32_t out_base = s_base + STAGES * kStageBytes;
+  Tail* st = reinterpret_cast<Tail*>(smem + STAGES * kStageBytes + Cfg<kFwd>::kOut);
+  volatile uint32_t* abort_flag = &st->abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_ctarank();
+  const VocabArgs& a = p.a;
+
+  if (tid == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(smem_u32(&st->full[s]), 1);     // the even CTA's expect; bytes of both CTAs
+      mbar_init(smem_u32(&st->empty[s]), 1);
     }
-    if (r >= n && kEpi != kDw && kEpi != kGrad) continue;
-    if (kEpi == kStats || kEpi == kGrad) {
-      const bool ok = r < n;
-      const int base = kEpi == kStats ? 0 : v0;
-      const int64_t tok = (ok && a.K) ? a.map[r] : 0;
-      for (int j = 0; j < 4; ++j) {
-        const int c = c0 + tx * 4 + j;
-        const int v = base + c;
-        float q = 0.0f;
-        if (kEpi == kGrad && ok && c < N)
-          q = exp2f(fmaf(acc[i][j], a.scale * kLog2e, -a.lse[r] * kLog2e));
-        if (ok && c < N) {
-          if (a.K == 0) {
-            if (a.tgt[r] == v) {
-              if (kEpi == kStats) a.zt[r] = acc[i][j];
-              q -= 1.0f;
-            }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&st->tfull[b]), 1);
+      mbar_init(smem_u32(&st->tempty[b]), 2 * kEpiWarps);
+    }
+    st->abort_flag = 0;
+    mbar_fence_init();
+  }
+  grid_dependency_wait();
+  // both CTAs' barriers exist before either CTA's work refers to them
+  __syncthreads();
+  cluster_arrive();
+  cluster_wait();
+  if (warp == 1) tmem_alloc_pair(smem_u32(&st->tmem_base), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = st->tmem_base;
+  const int n = *a.n_rows;
+  const Schedule sch = make_schedule<kFwd>(p, n, (int)(blockIdx.x >> 1), (int)(gridDim.x >> 1));
+
+  if (warp == 0) {
+    // ------------------------------------------------------- TMA producer --
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool alive = true;
+      const int half = (int)rank * 128;
+      Job j;
+      for (int i = 0; alive && get_job<kFwd>(p, sch, n, i, &j); ++i) {
+        for (int k = 0; k < j.steps; ++k, ++it) {
+          const int s = it % STAGES;
+          if (!mbar_wait(smem_u32(&st->empty[s]), ((it / STAGES) & 1u) ^ 1u, abort_flag, a.status, 51)) {
+            alive = false;
+            break;
+          }
+          const uint32_t fb = mapa(smem_u32(&st->full[s]), 0);
+          if (rank == 0) mbar_expect_tx(smem_u32(&st->full[s]), 2 * kStageBytes);
+          const uint32_t da = s_base + s * kStageBytes, db = da + kOperand;
+          const int kk = j.k0 + k * kBK;
+          if (kFwd || j.kind == kGrad) {
+            tma_load_2d_pair(da, &p.x_k, fb, kk, j.a0 + half);
+            tma_load_2d_pair(db, &p.w_k, fb, kk, (kFwd ? 0 : p.v_grad) + j.b0 + half);
+          } else if (j.kind == kDx) {
+            tma_load_2d_pair(da, &p.g_k, fb, kk, j.a0 + half);
+            tma_load_2d_pair(db, &p.w_mn, fb, j.b0 + half, p.v_prod + kk);
+            tma_load_2d_pair(db + kOperand / 2, &p.w_mn, fb, j.b0 + half + 64, p.v_prod + kk);
           } else {
-            for (int k = 0; k < a.K; ++k)
-              if (a.ids[tok * a.K + k] == v) {
-                if (kEpi == kStats) a.zt[(int64_t)r * a.K + k] = acc[i][j];
-                q -= a.p[tok * a.K + k];
-              }
+            tma_load_2d_pair(da, &p.g_mn, fb, j.a0 + half, kk);
+            tma_load_2d_pair(da + kOperand / 2, &p.g_mn, fb, j.a0 + half + 64, kk);
+            tma_load_2d_pair(db, &p.x_mn, fb, j.b0 + half, kk);
+            tma_load_2d_pair(db + kOperand / 2, &p.x_mn, fb, j.b0 + half + 64, kk);
           }
         }
-        if (kEpi == kGrad && c < a.ldg)
-          a.g[(int64_t)r * a.ldg + c] = __float2bfloat16_rn(ok && c < N ? a.gcoef[r] * q : 0.0f);
       }
-    } else {
-      for (int j = 0; j < 4; ++j) {
-        const int c = c0 + tx * 4 + j;
-        if (r >= M || c >= N) continue;
-        if (kEpi == kDx) {
-          float* d = a.dx + (int64_t)r * a.H + c;
-          *d = first ? acc[i][j] : *d + acc[i][j];
-        } else {
-          a.dw[(int64_t)(v0 + r) * a.H + c] = __float2bfloat16_rn(acc[i][j]);
+      // this CTA's last stage release must have landed before it can exit
+      if (alive && it)
+        mbar_drain(smem_u32(&st->empty[(it - 1) % STAGES]), ((it - 1) / STAGES) & 1u, a.status, 56);
+      if (!alive) {
+        // The copies already issued count on the even CTA's barriers, which
+        // may never complete now: give them time to land before leaving.
+        const uint64_t t0 = gtimer();
+        while (gtimer() - t0 < 2000000ull) {
         }
       }
     }
-  }
-  if (kEpi == kStats) {
-    __syncthreads();
-    if (tid < kT && m0 + tid < n) {
-      float s = 0.0f, cnt = 0.0f;
-      for (int j = 0; j < 16; ++j) s += red[tid][j];
-      for (int j = 0; j < 16; ++j) cnt += ties[tid][j];
-      s += cnt - 1.0f;
-      a.part[(int64_t)blockIdx.x * a.rows_pad + m0 + tid] = make_float2(red[tid][16], s);
+    __syncwarp();
+  } else if (warp == 1) {
+    // --------------------------------------------------------- MMA issuer --
+    if (lane == 0 && rank == 0) {
+      uint32_t it = 0, use = 0;      // steps; uses of a TMEM buffer
+      bool alive = true;
+      Job j;
+      for (int i = 0; alive && get_job<kFwd>(p, sch, n, i, &j); ++i) {
+        const bool a_mn = !kFwd && j.kind == kDw;
+        const bool b_mn = !kFwd && j.kind >= kDx;
+        const uint32_t id = kIdesc | (a_mn ? kMnA : 0u) | (b_mn ? kMnB : 0u);
+        for (int k = 0; k < j.steps; ++k, ++it) {
+          const bool fresh = k == 0 || (kFwd && k % kRun == 0);
+          const bool last = k + 1 == j.steps || (kFwd && (k + 1) % kRun == 0);
+          const uint32_t buf = use & 1u;
+          const int s = it % STAGES;
+          if ((fresh && !mbar_wait(smem_u32(&st->tempty[buf]), ((use >> 1) & 1u) ^ 1u, abort_flag,
+                                   a.status, 52)) ||
+              !mbar_wait(smem_u32(&st->full[s]), (it / STAGES) & 1u, abort_flag, a.status, 53)) {
+            alive = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem_base + buf * kTile;
+          const uint32_t sa = s_base + s * kStageBytes, sb = sa + kOperand;
+#pragma unroll
+          for (int q = 0; q < kBK / 16; ++q) {
+            // 16 deep: 32 bytes along a K-major row, 16 rows of an MN-major block
+            const uint64_t da = a_mn ? sw128_desc_mn(sa + q * 2048, kOperand / 2) : sw128_desc(sa + q * 32);
+            const uint64_t db = b_mn ? sw128_desc_mn(sb + q * 2048, kOperand / 2) : sw128_desc(sb + q * 32);
+            mma_f16_pair(d, da, db, id, (fresh && q == 0) ? 0u : 1u);
+          }
+          mma_commit_pair(smem_u32(&st->empty[s]));
+          if (last) {
+            mma_commit_pair(smem_u32(&st->tfull[buf]));
+            ++use;
+          }
+        }
+      }
     }
+    __syncwarp();
+  } else {
+    // ----------------------------------------------------------- epilogue --
+    const int q = warp & 3;                  // TMEM lane quarter of this warp
+    const int h = (warp - 2) >> 2;           // column half
+    const uint32_t tm = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * 128);
+    const uint32_t te[2] = {mapa(smem_u32(&st->tempty[0]), 0), mapa(smem_u32(&st->tempty[1]), 0)};
+    const uint32_t stg = out_base + (uint32_t)((warp - 2) * kStageOutBytes);
+    const float k2 = a.scale * kLog2e;
+    uint32_t use = 0;
+    bool alive = true;
+    Job j;
+    for (int i = 0; alive && get_job<kFwd>(p, sch, n, i, &j); ++i) {
+      const int row0 = j.a0 + (int)rank * 128 + q * 32;
+      const int row = row0 + lane;
+      const int col0 = j.b0 + h * 128;       // first column of this half
+      if constexpr (kFwd) {
+        // Runs of kRun steps are summed on the tensor cores and the runs added
+        // here, rounded to nearest: the tensor cores truncate every addition,
+        // a bias that grows with the length of the run.
+        const bool ok = row < n;
+        const int32_t tgt = (ok && a.K == 0) ? a.tgt[row] - col0 : -1;
+        const int32_t* ids = nullptr;
+        int cur = 0;
+        if (ok && a.K) {
+          ids = a.ids + (int64_t)a.map[row] * a.K;
+          cur = first_entry(ids, a.K, col0);
+        }
+        float acc[128];
+        for (int k = 0; k < j.steps; k += kRun, ++use) {
+          const uint32_t buf = use & 1u;
+          bool okw = mbar_wait(smem_u32(&st->tfull[buf]), (use >> 1) & 1u, abort_flag, a.status, 54);
+          okw = __all_sync(0xFFFFFFFFu, okw);
+          if (!okw) {
+            alive = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            tmem_ld32(tm + buf * kTile + c * 32, v);
+            tmem_wait_ld();
+            if (c == 3) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(te[buf]);
+            }
+            if (k == 0) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) acc[c * 32 + e] = __uint_as_float(v[e]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) acc[c * 32 + e] += __uint_as_float(v[e]);
+            }
+          }
+        }
+        if (!alive) break;
+        if (col0 < a.V) {
+          if (col0 + 128 > a.V) {
+#pragma unroll
+            for (int e = 0; e < 128; ++e)
+              if (col0 + e >= a.V) acc[e] = -INFINITY;
+          }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 128; ++e) mx = fmaxf(mx, acc[e]);
+          // The maximum's own term is 1: it is counted, not summed, so that
+          // what a nearly certain word leaves to the others keeps its bits.
+          const float base = mx == -INFINITY ? 0.0f : -mx * k2;
+          float s0 = 0.0f, s1 = 0.0f, ties = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 128; e += 2) {
+            const float e0 = exp2f(fmaf(acc[e], k2, base)), e1 = exp2f(fmaf(acc[e + 1], k2, base));
+            if (acc[e] == mx) ties += 1.0f; else s0 += e0;
+            if (acc[e + 1] == mx) ties += 1.0f; else s1 += e1;
+          }
+          const float rest = mx == -INFINITY ? s0 + s1 - 1.0f : s0 + s1 + (ties - 1.0f);
+          if (ok) a.part[(int64_t)(col0 / kVocabPart) * a.rows_pad + row] = make_float2(mx, rest);
+          if (__any_sync(0xFFFFFFFFu, tgt >= 0 && tgt < 128)) {
+            float z = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 128; ++e) z = tgt == e ? acc[e] : z;
+            if (tgt >= 0 && tgt < 128) a.zt[row] = z;
+          }
+          if (ids) {
+            for (; cur < a.K; ++cur) {
+              const int32_t rel = __ldg(ids + cur) - col0;
+              if (rel >= 128) break;
+              float z = 0.0f;
+#pragma unroll
+              for (int e = 0; e < 128; ++e) z = rel == e ? acc[e] : z;
+              a.zt[(int64_t)row * a.K + cur] = z;
+            }
+          }
+          __syncwarp();
+        }
+      } else {
+        const uint32_t buf = use & 1u;
+        // per-row constants of grad; loaded before the wait
+        const bool ok = row < n;
+        float gc = 0.0f, nl = 0.0f;
+        int32_t tgt = -1;
+        const int32_t* ids = nullptr;
+        const float* pr = nullptr;
+        int cur = 0;
+        const int vcol = p.v_grad + col0;    // grad: vocabulary column
+        if (j.kind == kGrad && ok) {
+          gc = a.gcoef[row];
+          nl = -a.lse[row] * kLog2e;
+          if (a.K == 0) {
+            tgt = a.tgt[row] - vcol;
+          } else {
+            const int64_t at = (int64_t)a.map[row] * a.K;
+            ids = a.ids + at;
+            pr = a.p + at;
+            cur = first_entry(ids, a.K, vcol);
+          }
+        }
+        bool okw = mbar_wait(smem_u32(&st->tfull[buf]), (use >> 1) & 1u, abort_flag, a.status, 55);
+        okw = __all_sync(0xFFFFFFFFu, okw);
+        if (!okw) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+        ++use;
+        // the previous job's stores have read the staging buffer
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tmem_ld32(tm + buf * kTile + c * 32, v);
+          tmem_wait_ld();
+          if (c == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(te[buf]);
+          }
+          if (j.kind == kDx) {
+            // FP32 boxes of 32 columns; two in flight
+            const uint32_t box = stg + (c & 1) * kBoxBytes;
+            if (c >= 2) {
+              if (lane == 0) bulk_wait_read_1();
+              __syncwarp();
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              st_shared_v4(box + (uint32_t)(lane * 128 + ((e ^ (lane & 7)) * 16)), v[e * 4], v[e * 4 + 1],
+                           v[e * 4 + 2], v[e * 4 + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              const int col = col0 + c * 32;
+              if (col < a.H) {
+                const int r = j.slice * a.rows_pad + row0;
+                if (p.dx_first)
+                  tma_store_2d(&p.dx_out, box, col, r);
+                else
+                  tma_add_2d(&p.dx_out, box, col, r);
+              }
+              bulk_commit();
+            }
+          } else {
+            float f[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[e]);
+            if (j.kind == kGrad) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) f[e] = exp2f(fmaf(f[e], k2, nl));
+              const int32_t rel = tgt - c * 32;
+              if (__any_sync(0xFFFFFFFFu, rel >= 0 && rel < 32)) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) f[e] = rel == e ? f[e] - 1.0f : f[e];
+              }
+              if (ids) {
+                for (; cur < a.K; ++cur) {
+                  const int32_t re = __ldg(ids + cur) - vcol - c * 32;
+                  if (re >= 32) break;
+                  const float pp = __ldg(pr + cur);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) f[e] = re == e ? f[e] - pp : f[e];
+                }
+              }
+              __syncwarp();
+              const int live = ok ? a.V - (vcol + c * 32) : 0;   // columns that exist
+#pragma unroll
+              for (int e = 0; e < 32; ++e) f[e] = e < live ? gc * f[e] : 0.0f;
+            }
+            // BF16 boxes of 64 columns
+            const uint32_t box = stg + (c >> 1) * kBoxBytes;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              __nv_bfloat162 b0 = __floats2bfloat162_rn(f[e * 8], f[e * 8 + 1]);
+              __nv_bfloat162 b1 = __floats2bfloat162_rn(f[e * 8 + 2], f[e * 8 + 3]);
+              __nv_bfloat162 b2 = __floats2bfloat162_rn(f[e * 8 + 4], f[e * 8 + 5]);
+              __nv_bfloat162 b3 = __floats2bfloat162_rn(f[e * 8 + 6], f[e * 8 + 7]);
+              const int chunk = (c & 1) * 4 + e;
+              st_shared_v4(box + (uint32_t)(lane * 128 + ((chunk ^ (lane & 7)) * 16)),
+                           *reinterpret_cast<uint32_t*>(&b0), *reinterpret_cast<uint32_t*>(&b1),
+                           *reinterpret_cast<uint32_t*>(&b2), *reinterpret_cast<uint32_t*>(&b3));
+            }
+            if (c & 1) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                const int col = col0 + (c >> 1) * 64;
+                if (j.kind == kGrad) {
+                  tma_store_2d(&p.g_out, box, col, row0);
+                } else if (col < a.H && p.v_prod + row0 < a.V) {
+                  tma_store_2d(&p.dw_out, box, col, p.v_prod + row0);
+                }
+                bulk_commit();
+              }
+            }
+          }
+        }
+      }
+    }
+    if (!kFwd && lane == 0) bulk_wait_all();   // this warp's tensor stores are complete
+  }
+
+  // Nothing of either CTA is used by the other any more, and every result has
+  // been read, before tensor memory is freed and the CTAs leave.
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive();
+  cluster_wait();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
   }
 }
 
-inline unsigned up(int64_t x) { return (unsigned)((x + kT - 1) / kT); }
+// ------------------------------------------------------------------- host --
+
+fp8rl_status map_bf16(CUtensorMap* m, const void* base, int64_t inner, int64_t rows, int64_t ld,
+                      uint32_t box_rows, const char* what) {
+  return encode_tiled_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, (uint64_t)inner, (uint64_t)rows,
+                         (uint64_t)ld * 2, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B, what);
+}
+
+// Sets the shared-memory attribute once per device and asks how many CTA
+// pairs are resident at once (an SM without a partner in its cluster stays idle).
+template <bool kFwd>
+fp8rl_status pairs_of(const DeviceState* ds, int* pairs) {
+  static int cache[64] = {0};
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lock(mu);
+  int& c = cache[ds->device & 63];
+  if (c == 0) {
+    const size_t bytes = smem_bytes<kFwd>();
+    if ((size_t)ds->max_smem_optin < bytes)
+      return fail(FP8RL_ERR_UNSUPPORTED_DEVICE, "needs %zu bytes of shared memory per block", bytes);
+    fp8rl_status st = cuda_check(
+        cudaFuncSetAttribute(vocab_kernel<kFwd>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes),
+        "cudaFuncSetAttribute(vocab)");
+    if (st != FP8RL_OK) return st;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(ds->sm_count & ~1));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int got = 0;
+    st = cuda_check(cudaOccupancyMaxActiveClusters(&got, vocab_kernel<kFwd>, &cfg),
+                    "cudaOccupancyMaxActiveClusters(vocab)");
+    if (st != FP8RL_OK) return st;
+    if (got < 1) return fail(FP8RL_ERR_UNSUPPORTED_DEVICE, "no CTA pair fits on the device");
+    c = got;
+  }
+  *pairs = c;
+  return FP8RL_OK;
+}
+
+template <bool kFwd>
+fp8rl_status launch(const Params& p, int64_t jobs_most, const DeviceState* ds, cudaStream_t stream) {
+  int pairs = 0;
+  const fp8rl_status st = pairs_of<kFwd>(ds, &pairs);
+  if (st != FP8RL_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(jobs_most, pairs)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<kFwd>();
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_check(cudaLaunchKernelEx(&cfg, vocab_kernel<kFwd>, p), "vocab_kernel launch");
+}
+
+inline int64_t tiles(int64_t x) { return (x + kTile - 1) / kTile; }
 
 }  // namespace
 
-fp8rl_status vocab_forward(const VocabArgs& a, const DeviceState*, cudaStream_t stream) {
-  const Operand A = {a.x, a.H, 1}, B = {a.w, a.ldw, 1};
-  vocab_gemm_kernel<kStats><<<dim3(up(a.V), up(a.rows_cap)), 256, 0, stream>>>(a, A, B, 0, a.V, 0);
-  return cuda_check(cudaGetLastError(), "vocab_gemm_kernel launch");
+int vocab_dx_slices(int64_t rows, int64_t H, int64_t vc) {
+  // at least about two dX jobs per pair of SMs, each at least 8 steps deep
+  const int64_t base = tiles(rows) * tiles(H);
+  const int64_t want = (152 + base - 1) / base;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(want, vc / (8 * kBK)));
 }
 
-fp8rl_status vocab_backward_piece(const VocabArgs& a, int v0, int vc, bool first,
-                                  const DeviceState*, cudaStream_t stream) {
-  const Operand X = {a.x, a.H, 1}, W = {a.w + (int64_t)v0 * a.ldw, a.ldw, 1};
-  vocab_gemm_kernel<kGrad>
-      <<<dim3(up(vc), up(a.rows_pad)), 256, 0, stream>>>(a, X, W, v0, vc, 0);
+fp8rl_status vocab_forward(const VocabArgs& a, const DeviceState* ds, cudaStream_t stream) {
+  Params p = {};
+  p.a = a;
+  fp8rl_status st;
+  if ((st = map_bf16(&p.x_k, a.x, a.H, a.rows_pad, a.H, 128, "hidden")) != FP8RL_OK) return st;
+  if ((st = map_bf16(&p.w_k, a.w, a.H, a.V, a.ldw, 128, "weight")) != FP8RL_OK) return st;
+  return launch<true>(p, tiles(a.rows_cap) * tiles(a.V), ds, stream);
+}
+
+fp8rl_status vocab_backward(const VocabArgs& a, const DeviceState* ds, cudaStream_t stream) {
+  Params p = {};
+  p.a = a;
+  fp8rl_status st;
+  if ((st = map_bf16(&p.x_k, a.x, a.H, a.rows_pad, a.H, 128, "hidden")) != FP8RL_OK) return st;
+  if ((st = map_bf16(&p.w_k, a.w, a.H, a.V, a.ldw, 128, "weight")) != FP8RL_OK) return st;
+  if ((st = map_bf16(&p.x_mn, a.x, a.H, a.rows_pad, a.H, 64, "hidden")) != FP8RL_OK) return st;
+  if ((st = map_bf16(&p.w_mn, a.w, a.H, a.V, a.ldw, 64, "weight")) != FP8RL_OK) return st;
+  CUtensorMap g_out[2], g_k[2], g_mn[2];
+  for (int i = 0; i < 2; ++i) {
+    const void* g = a.g[i] ? a.g[i] : a.g[0];
+    if ((st = map_bf16(&g_out[i], g, a.vc, a.rows_pad, a.vc, 32, "G")) != FP8RL_OK) return st;
+    if ((st = map_bf16(&g_k[i], g, a.vc, a.rows_pad, a.vc, 128, "G")) != FP8RL_OK) return st;
+    if ((st = map_bf16(&g_mn[i], g, a.vc, a.rows_pad, a.vc, 64, "G")) != FP8RL_OK) return st;
+  }
   if (a.dx) {
-    const Operand G = {a.g, a.ldg, 1}, Wt = {W.p, 1, a.ldw};
-    vocab_gemm_kernel<kDx>
-        <<<dim3(up(a.H), up(a.rows_cap)), 256, 0, stream>>>(a, G, Wt, v0, vc, first);
+    if ((st = encode_tiled_2d(&p.dx_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.dx, (uint64_t)a.H,
+                              (uint64_t)a.slices * a.rows_pad, (uint64_t)a.H * 4, 32, 32,
+                              CU_TENSOR_MAP_SWIZZLE_128B, "dX")) != FP8RL_OK)
+      return st;
+  } else {
+    p.dx_out = p.x_k;
   }
   if (a.dw) {
-    const Operand Gt = {a.g, 1, a.ldg}, Xt = {a.x, 1, a.H};
-    vocab_gemm_kernel<kDw><<<dim3(up(a.H), up(vc)), 256, 0, stream>>>(a, Gt, Xt, v0, vc, 0);
+    if ((st = map_bf16(&p.dw_out, a.dw, a.H, a.V, a.H, 32, "grad_weight")) != FP8RL_OK) return st;
+  } else {
+    p.dw_out = p.x_k;
   }
-  return cuda_check(cudaGetLastError(), "vocab_gemm_kernel launch");
+  // launch i: G of piece i, dX and dW of piece i - 1
+  const int64_t pieces = (a.V + a.vc - 1) / a.vc;
+  const int64_t mt = tiles(a.rows_cap), ht = tiles(a.H);
+  for (int64_t i = 0; i <= pieces; ++i) {
+    int64_t jobs = 0;
+    p.n_grad = p.dx_tiles_n = p.dw_tiles_n = 0;
+    p.vc_prod = 0;
+    if (i < pieces) {
+      p.v_grad = (int)(i * a.vc);
+      p.n_grad = (int)tiles(std::min<int64_t>(a.vc, a.V - p.v_grad));
+      p.g_out = g_out[i & 1];
+      jobs += mt * p.n_grad;
+    }
+    if (i > 0) {
+      p.v_prod = (int)((i - 1) * a.vc);
+      p.vc_prod = (int)std::min<int64_t>(a.vc, a.V - p.v_prod);
+      p.g_k = g_k[(i - 1) & 1];
+      p.g_mn = g_mn[(i - 1) & 1];
+      p.dx_first = i == 1;
+      if (a.dx) {
+        p.dx_tiles_n = (int)ht;
+        jobs += mt * ht * a.slices;
+      }
+      if (a.dw) {
+        p.dw_tiles_n = (int)ht;
+        jobs += tiles(p.vc_prod) * ht;
+      }
+    }
+    if ((st = launch<false>(p, jobs, ds, stream)) != FP8RL_OK) return st;
+  }
+  return FP8RL_OK;
 }
 
 }  // namespace fp8rl
