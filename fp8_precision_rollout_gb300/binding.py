@@ -509,47 +509,74 @@ def vocab_workspace_bytes(tokens: int, hidden_dim: int, vocab: int, top_k: int =
                                                   int(top_k), 1 if backward else 0))
 
 
+# The calls below can take less time on the GPU than checks and allocations take
+# here, so a tensor is looked at once, and only a bad one a second time to name
+# what is wrong with it.
+
 def _head(hidden, weight):
-    _rowmajor(_dev(hidden, torch.bfloat16, "hidden"), "hidden")
-    _rowmajor(_dev(weight, torch.bfloat16, "weight"), "weight")
-    if hidden.shape[1] != weight.shape[1]:
+    if not (hidden.is_cuda and weight.is_cuda and hidden.dtype is torch.bfloat16
+            and weight.dtype is torch.bfloat16 and hidden.dim() == 2 and weight.dim() == 2
+            and hidden.stride(1) == 1 and weight.stride(1) == 1):
+        _rowmajor(_dev(hidden, torch.bfloat16, "hidden"), "hidden")
+        _rowmajor(_dev(weight, torch.bfloat16, "weight"), "weight")
+    t, h = hidden.shape
+    v, hw = weight.shape
+    if h != hw:
         raise ValueError("hidden [tokens, hidden_dim] and weight [vocab, hidden_dim] must agree")
-    return hidden.shape[0], hidden.shape[1], weight.shape[0]
-
-
-def _row_stride(t):
+    if weight.get_device() != hidden.get_device():
+        raise ValueError("hidden and weight must be on one device")
     # the stride of a single row says nothing (torch may report any value)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t, h, v, (hidden.stride(0) if t > 1 else h), (weight.stride(0) if v > 1 else h)
 
 
 def _dense(t, dtype, shape, like, name):
-    _dev(t, dtype, name)
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != like.device:
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous() and t.get_device() == like.get_device()):
+        _dev(t, dtype, name)
         raise ValueError("%s must be a dense %s tensor on %s" % (name, list(shape), like.device))
-    return t
+    return t.data_ptr()
 
 
-def _head_workspace(workspace, t, h, v, k, backward, like, stream):
+def _head_stream(stream, like):
+    """(raw stream, whether it is the device's current one)."""
+    current = torch._C._cuda_getCurrentRawStream(like.get_device())
+    if stream is None:
+        return current, True
+    s = _stream(stream)
+    return s, s == current
+
+
+def _head_workspace(workspace, t, h, v, k, backward, like, stream, is_current):
     if workspace is None:
-        workspace = torch.empty(max(1, vocab_workspace_bytes(t, h, v, k, backward)),
-                                dtype=torch.uint8, device=like.device)
-        if stream != torch.cuda.current_stream(like.device).cuda_stream:
+        need = load().fp8rl_vocab_workspace_bytes(t, h, v, k, backward)
+        workspace = torch.empty(max(1, need), dtype=torch.uint8, device=like.device)
+        if not is_current:
             # freed on return: the allocator must know the stream that still uses it
             workspace.record_stream(torch.cuda.ExternalStream(stream, device=like.device))
+        return workspace, need
+    return workspace, _workspace_size(workspace, like)
+
+
+def _workspace_size(workspace, like):
     _dev(workspace, torch.uint8, "workspace")
-    if not workspace.is_contiguous() or workspace.device != like.device:
+    if not workspace.is_contiguous() or workspace.get_device() != like.get_device():
         raise ValueError("workspace must be a contiguous tensor on %s" % like.device)
-    return workspace
+    return workspace.numel()
+
+
+def _head_out(out, shape, dtype, like, name):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _dense(out, dtype, shape, like, name)
+    return out
 
 
 def _teacher_entries(teacher_ids, teacher_logits, t, like):
-    _dev(teacher_ids, torch.int32, "teacher_ids")
-    if teacher_ids.dim() != 2:
-        raise ValueError("teacher_ids must be [tokens, top_k]")
+    if not isinstance(teacher_ids, torch.Tensor) or teacher_ids.dim() != 2:
+        raise ValueError("teacher_ids must be a [tokens, top_k] tensor")
     k = teacher_ids.shape[1]
-    _dense(teacher_ids, torch.int32, (t, k), like, "teacher_ids")
-    _dense(teacher_logits, torch.float32, (t, k), like, "teacher_logits")
-    return k
+    return (k, _dense(teacher_ids, torch.int32, (t, k), like, "teacher_ids"),
+            _dense(teacher_logits, torch.float32, (t, k), like, "teacher_logits"))
 
 
 def token_logprobs(hidden, weight, targets, logit_scale: float = 1.0,
@@ -558,33 +585,23 @@ def token_logprobs(hidden, weight, targets, logit_scale: float = 1.0,
     """Log-probability of targets int32 [T] under softmax(logit_scale * hidden @ weight^T)
     (bf16 hidden [T, H], weight [V, H]) and the log-sum-exp, float32 [T] each:
     (logp, lse).  Tokens with a negative target are left out (0, 0)."""
-    t, h, v = _head(hidden, weight)
-    _dense(targets, torch.int32, (t,), hidden, "targets")
-    if logp is None:
-        logp = torch.empty(t, dtype=torch.float32, device=hidden.device)
-    if lse is None:
-        lse = torch.empty(t, dtype=torch.float32, device=hidden.device)
-    _dense(logp, torch.float32, (t,), hidden, "logp")
-    _dense(lse, torch.float32, (t,), hidden, "lse")
-    s = _stream(stream)
-    ws = _head_workspace(workspace, t, h, v, 0, False, hidden, s)
-    _check(load().fp8rl_token_logprobs(hidden.data_ptr(), _row_stride(hidden), weight.data_ptr(),
-                                       _row_stride(weight), targets.data_ptr(), t, h, v,
-                                       float(logit_scale), logp.data_ptr(), lse.data_ptr(),
-                                       ws.data_ptr(), ws.numel(), s))
+    t, h, v, ldh, ldw = _head(hidden, weight)
+    tp = _dense(targets, torch.int32, (t,), hidden, "targets")
+    logp = _head_out(logp, (t,), torch.float32, hidden, "logp")
+    lse = _head_out(lse, (t,), torch.float32, hidden, "lse")
+    s, current = _head_stream(stream, hidden)
+    ws, size = _head_workspace(workspace, t, h, v, 0, 0, hidden, s, current)
+    _check(load().fp8rl_token_logprobs(hidden.data_ptr(), ldh, weight.data_ptr(), ldw, tp, t, h, v,
+                                       logit_scale, logp.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+                                       size, s))
     return logp, lse
 
 
-def _head_gradients(hidden, weight, grad_hidden, grad_weight, need_hidden, need_weight):
-    t, h, v = hidden.shape[0], hidden.shape[1], weight.shape[0]
-    if grad_hidden is None and need_hidden:
-        grad_hidden = torch.empty(t, h, dtype=torch.bfloat16, device=hidden.device)
-    if grad_weight is None and need_weight:
-        grad_weight = torch.empty(v, h, dtype=torch.bfloat16, device=hidden.device)
-    if grad_hidden is not None:
-        _dense(grad_hidden, torch.bfloat16, (t, h), hidden, "grad_hidden")
-    if grad_weight is not None:
-        _dense(grad_weight, torch.bfloat16, (v, h), hidden, "grad_weight")
+def _head_gradients(hidden, weight, t, h, v, grad_hidden, grad_weight, need_hidden, need_weight):
+    if grad_hidden is not None or need_hidden:
+        grad_hidden = _head_out(grad_hidden, (t, h), torch.bfloat16, hidden, "grad_hidden")
+    if grad_weight is not None or need_weight:
+        grad_weight = _head_out(grad_weight, (v, h), torch.bfloat16, hidden, "grad_weight")
     return grad_hidden, grad_weight
 
 
@@ -596,18 +613,18 @@ def token_logprobs_backward(hidden, weight, targets, lse, grad_logp, logit_scale
     """Gradients (bf16 grad_hidden [T, H], grad_weight [V, H]) of
     sum(grad_logp * logp), with the lse token_logprobs returned.  An output
     that is neither given nor needed is not computed (None)."""
-    t, h, v = _head(hidden, weight)
-    _dense(targets, torch.int32, (t,), hidden, "targets")
-    _dense(lse, torch.float32, (t,), hidden, "lse")
-    _dense(grad_logp, torch.float32, (t,), hidden, "grad_logp")
-    gh, gw = _head_gradients(hidden, weight, grad_hidden, grad_weight, need_hidden, need_weight)
-    s = _stream(stream)
-    ws = _head_workspace(workspace, t, h, v, 0, True, hidden, s)
+    t, h, v, ldh, ldw = _head(hidden, weight)
+    tp = _dense(targets, torch.int32, (t,), hidden, "targets")
+    lp = _dense(lse, torch.float32, (t,), hidden, "lse")
+    gp = _dense(grad_logp, torch.float32, (t,), hidden, "grad_logp")
+    gh, gw = _head_gradients(hidden, weight, t, h, v, grad_hidden, grad_weight, need_hidden,
+                             need_weight)
+    s, current = _head_stream(stream, hidden)
+    ws, size = _head_workspace(workspace, t, h, v, 0, 1, hidden, s, current)
     _check(load().fp8rl_token_logprobs_backward(
-        hidden.data_ptr(), _row_stride(hidden), weight.data_ptr(), _row_stride(weight),
-        targets.data_ptr(), lse.data_ptr(), grad_logp.data_ptr(), t, h, v, float(logit_scale),
-        gh.data_ptr() if gh is not None else None, gw.data_ptr() if gw is not None else None,
-        ws.data_ptr(), ws.numel(), s))
+        hidden.data_ptr(), ldh, weight.data_ptr(), ldw, tp, lp, gp, t, h, v, logit_scale,
+        None if gh is None else gh.data_ptr(), None if gw is None else gw.data_ptr(),
+        ws.data_ptr(), size, s))
     return gh, gw
 
 
@@ -618,20 +635,15 @@ def distill_topk(hidden, weight, teacher_ids, teacher_logits, logit_scale: float
     int32 [T, K], teacher_logits float32 [T, K]; id < 0 or logit -inf: absent)
     to the student softmax(logit_scale * hidden @ weight^T), and the student's
     log-sum-exp: (loss, lse).  Tokens without entries are left out (0, 0)."""
-    t, h, v = _head(hidden, weight)
-    k = _teacher_entries(teacher_ids, teacher_logits, t, hidden)
-    if loss is None:
-        loss = torch.empty(t, dtype=torch.float32, device=hidden.device)
-    if lse is None:
-        lse = torch.empty(t, dtype=torch.float32, device=hidden.device)
-    _dense(loss, torch.float32, (t,), hidden, "loss")
-    _dense(lse, torch.float32, (t,), hidden, "lse")
-    s = _stream(stream)
-    ws = _head_workspace(workspace, t, h, v, k, False, hidden, s)
-    _check(load().fp8rl_distill_topk(hidden.data_ptr(), _row_stride(hidden), weight.data_ptr(),
-                                     _row_stride(weight), teacher_ids.data_ptr(),
-                                     teacher_logits.data_ptr(), k, t, h, v, float(logit_scale),
-                                     loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), s))
+    t, h, v, ldh, ldw = _head(hidden, weight)
+    k, ip, up = _teacher_entries(teacher_ids, teacher_logits, t, hidden)
+    loss = _head_out(loss, (t,), torch.float32, hidden, "loss")
+    lse = _head_out(lse, (t,), torch.float32, hidden, "lse")
+    s, current = _head_stream(stream, hidden)
+    ws, size = _head_workspace(workspace, t, h, v, k, 0, hidden, s, current)
+    _check(load().fp8rl_distill_topk(hidden.data_ptr(), ldh, weight.data_ptr(), ldw, ip, up, k, t,
+                                     h, v, logit_scale, loss.data_ptr(), lse.data_ptr(),
+                                     ws.data_ptr(), size, s))
     return loss, lse
 
 
@@ -643,18 +655,18 @@ def distill_topk_backward(hidden, weight, teacher_ids, teacher_logits, lse, grad
     """Gradients (bf16 grad_hidden [T, H], grad_weight [V, H]) of
     sum(grad_loss * loss), with the lse distill_topk returned; outputs as in
     token_logprobs_backward."""
-    t, h, v = _head(hidden, weight)
-    k = _teacher_entries(teacher_ids, teacher_logits, t, hidden)
-    _dense(lse, torch.float32, (t,), hidden, "lse")
-    _dense(grad_loss, torch.float32, (t,), hidden, "grad_loss")
-    gh, gw = _head_gradients(hidden, weight, grad_hidden, grad_weight, need_hidden, need_weight)
-    s = _stream(stream)
-    ws = _head_workspace(workspace, t, h, v, k, True, hidden, s)
+    t, h, v, ldh, ldw = _head(hidden, weight)
+    k, ip, up = _teacher_entries(teacher_ids, teacher_logits, t, hidden)
+    lp = _dense(lse, torch.float32, (t,), hidden, "lse")
+    gp = _dense(grad_loss, torch.float32, (t,), hidden, "grad_loss")
+    gh, gw = _head_gradients(hidden, weight, t, h, v, grad_hidden, grad_weight, need_hidden,
+                             need_weight)
+    s, current = _head_stream(stream, hidden)
+    ws, size = _head_workspace(workspace, t, h, v, k, 1, hidden, s, current)
     _check(load().fp8rl_distill_topk_backward(
-        hidden.data_ptr(), _row_stride(hidden), weight.data_ptr(), _row_stride(weight),
-        teacher_ids.data_ptr(), teacher_logits.data_ptr(), k, lse.data_ptr(), grad_loss.data_ptr(),
-        t, h, v, float(logit_scale), gh.data_ptr() if gh is not None else None,
-        gw.data_ptr() if gw is not None else None, ws.data_ptr(), ws.numel(), s))
+        hidden.data_ptr(), ldh, weight.data_ptr(), ldw, ip, up, k, lp, gp, t, h, v, logit_scale,
+        None if gh is None else gh.data_ptr(), None if gw is None else gw.data_ptr(),
+        ws.data_ptr(), size, s))
     return gh, gw
 
 

@@ -122,6 +122,13 @@ __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// Lets the next grid in the stream, if it allows programmatic serialization,
+// start its prologue once every CTA of this grid has got here; its memory
+// accesses still come after its own grid_dependency_wait.
+__device__ __forceinline__ void grid_dependents_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ------------------------------------------------- clusters / DSMEM ------
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {

@@ -26,6 +26,7 @@
 #include <climits>
 #include <cmath>
 
+#include "sm100_ptx.cuh"
 #include "vocab.h"
 
 namespace fp8rl {
@@ -57,6 +58,8 @@ __global__ void __launch_bounds__(kTeacherWarps * 32)
   __shared__ float su[kTeacherWarps][kMaxTopK];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t = (int64_t)blockIdx.x * kTeacherWarps + warp;
+  ptx::grid_dependents_launch();
+  ptx::grid_dependency_wait();
   if (t >= T) return;
   int32_t* id = sid[warp];
   float* u = su[warp];
@@ -124,6 +127,8 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsArgs a) {
   __shared__ int idx[kRowThreads];
   __shared__ int sbase;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  ptx::grid_dependents_launch();
+  ptx::grid_dependency_wait();
   const int64_t r0 = (int64_t)blockIdx.x * a.rows_per_cta;
   const int64_t r1 = min(a.T, r0 + a.rows_per_cta);
   int before = 0;
@@ -171,16 +176,14 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsArgs a) {
     base += total;
     __syncthreads();
     const int here = (int)min((int64_t)kRowThreads, r1 - c0);
-    for (int r = warp; r < here; r += kRowThreads / 32) {
+    for (int i = tid; i < here * vecs; i += kRowThreads) {
+      const int r = i / vecs, v = i - r * vecs;
       const int dst = idx[r];
-      if (dst >= 0) {
-        const uint4* src = reinterpret_cast<const uint4*>(a.hidden + (c0 + r) * a.ldh);
-        uint4* to = reinterpret_cast<uint4*>(a.x + (int64_t)dst * a.H);
-        for (int v = lane; v < vecs; v += 32) to[v] = __ldg(src + v);
-      } else if (a.grad_hidden) {
-        uint4* to = reinterpret_cast<uint4*>(a.grad_hidden + (c0 + r) * a.H);
-        for (int v = lane; v < vecs; v += 32) to[v] = make_uint4(0, 0, 0, 0);
-      }
+      if (dst >= 0)
+        reinterpret_cast<uint4*>(a.x + (int64_t)dst * a.H)[v] =
+            __ldg(reinterpret_cast<const uint4*>(a.hidden + (c0 + r) * a.ldh) + v);
+      else if (a.grad_hidden)
+        reinterpret_cast<uint4*>(a.grad_hidden + (c0 + r) * a.H)[v] = make_uint4(0, 0, 0, 0);
     }
     __syncthreads();
   }
@@ -209,8 +212,8 @@ struct CombineArgs {
   float* lse;   // [T]
 };
 
-// Joins the softmax partial (m2, r2) into (m, r): a maximum and the sum of the
-// exponentials relative to it less the maximum's own 1.  Nothing: (-inf, -1).
+// Softmax partials (m, r): a maximum and the sum of the exponentials relative
+// to it less the maximum's own 1.  Nothing: (-inf, -1).  join adds (m2, r2).
 __device__ __forceinline__ void join(float& m, float& r, float m2, float r2, float k2) {
   const float d = (m2 - m) * k2;
   if (m2 > m) {
@@ -223,55 +226,88 @@ __device__ __forceinline__ void join(float& m, float& r, float m2, float r2, flo
   }
 }
 
-// Joins the softmax partials of 32 rows: 32 x 32 threads, lane = row, each
-// warp takes every 32nd part; then every warp the row's entries.  All sums
-// FP32 in a fixed order.
-__global__ void __launch_bounds__(1024) combine_kernel(const CombineArgs a) {
-  __shared__ float sm[32][33], ss[32][33];
+constexpr int kCombineThreads = 1024, kCombineBatch = 8;
+
+// Joins the partials of R rows (a power of two up to 32): thread = (part lane,
+// row), rows fastest, so that a warp reads R consecutive rows of 32 / R parts.
+// A thread loads kCombineBatch parts at once: with one after the other, the
+// chain of loads and exponentials took 22 us for one row of 1024 parts.  Then
+// across the part lanes, and one warp per row for the row's entries.  The
+// order of every sum depends on the sizes alone.
+template <int R>
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineArgs a) {
+  __shared__ float sm[32][R], sr[32][R];
+  ptx::grid_dependents_launch();
+  ptx::grid_dependency_wait();
   const int n = *a.n_rows;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  if (blockIdx.x * 32 >= n) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int c0 = blockIdx.x * R;
+  if (c0 >= n) return;
+  constexpr int kLanes = kCombineThreads / R;
   const float k2 = a.scale * 1.4426950408889634f;
-  const bool ok = c < n;
   float m = -INFINITY, r = -1.0f;
-  if (ok) {
-#pragma unroll 4
-    for (int i = warp; i < a.parts; i += 32) {
-      const float2 q = a.part[(int64_t)i * a.rows_pad + c];
-      join(m, r, q.x, q.y, k2);
+  const int c = c0 + tid % R;
+  if (c < n) {
+    for (int i = tid / R; i < a.parts; i += kLanes * kCombineBatch) {
+      float2 q[kCombineBatch];
+#pragma unroll
+      for (int b = 0; b < kCombineBatch; ++b)
+        q[b] = i + b * kLanes < a.parts ? a.part[(int64_t)(i + b * kLanes) * a.rows_pad + c]
+                                        : make_float2(-INFINITY, -1.0f);
+      // pairwise: three dependent joins a batch
+#pragma unroll
+      for (int o = kCombineBatch / 2; o; o >>= 1)
+#pragma unroll
+        for (int b = 0; b < o; ++b) join(q[b].x, q[b].y, q[b + o].x, q[b + o].y, k2);
+      join(m, r, q[0].x, q[0].y, k2);
     }
   }
-  sm[warp][lane] = m;
-  ss[warp][lane] = r;
+#pragma unroll
+  for (int o = R; o < 32; o <<= 1) {
+    const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, o), r2 = __shfl_xor_sync(0xFFFFFFFFu, r, o);
+    // both lanes join (lower, higher), so that both hold the same bits
+    float ml = (lane & o) ? m2 : m, rl = (lane & o) ? r2 : r;
+    join(ml, rl, (lane & o) ? m : m2, (lane & o) ? r : r2, k2);
+    m = ml;
+    r = rl;
+  }
+  if (lane < R) {
+    sm[warp][lane] = m;
+    sr[warp][lane] = r;
+  }
   __syncthreads();
-  float top = -INFINITY, rest = -1.0f;
-  for (int i = 0; i < 32; ++i) join(top, rest, sm[i][lane], ss[i][lane], k2);
-  // Log-probabilities as (x - top) * scale - log(sum), the sum as 1 + rest: a
+  if (warp >= R || c0 + warp >= n) return;
+  const int row = c0 + warp;
+  m = sm[lane][warp];
+  r = sr[lane][warp];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, o), r2 = __shfl_xor_sync(0xFFFFFFFFu, r, o);
+    float ml = (lane & o) ? m2 : m, rl = (lane & o) ? r2 : r;
+    join(ml, rl, (lane & o) ? m : m2, (lane & o) ? r : r2, k2);
+    m = ml;
+    r = rl;
+  }
+  // Log-probabilities as (x - max) * scale - log(sum), the sum as 1 + rest: a
   // nearly certain word, whose log-probability is close to -rest, keeps its
   // relative accuracy, and a certain one has exactly 0.
-  const float ls = log1pf(rest);
-  const float lse = __fadd_rn(__fmul_rn(top, a.scale), ls);
-  __syncthreads();
-  float loss = 0.0f;
-  int64_t t = ok ? a.map[c] : 0;
-  if (ok && a.K) {
-    for (int k = warp; k < a.K; k += 32) {
-      const float p = a.p[t * a.K + k];
-      if (p != 0.0f) loss += p * (a.lp[t * a.K + k] -
-                     __fsub_rn(__fmul_rn(a.zt[(int64_t)c * a.K + k] - top, a.scale), ls));
-    }
-  }
-  sm[warp][lane] = loss;
-  __syncthreads();
-  if (warp != 0 || !ok) return;
-  a.lse[t] = lse;
+  const float ls = log1pf(r);
+  const int64_t t = a.map[row];
+  float out = 0.0f;
   if (a.K == 0) {
-    a.out[t] = __fsub_rn(__fmul_rn(a.zt[c] - top, a.scale), ls);
+    out = __fsub_rn(__fmul_rn(a.zt[row] - m, a.scale), ls);
   } else {
-    float l = 0.0f;
-    for (int i = 0; i < 32; ++i) l += sm[i][lane];
-    a.out[t] = l;
+    for (int k = lane; k < a.K; k += 32) {
+      const float p = a.p[t * a.K + k];
+      if (p != 0.0f)
+        out += p * (a.lp[t * a.K + k] -
+                    __fsub_rn(__fmul_rn(a.zt[(int64_t)row * a.K + k] - m, a.scale), ls));
+    }
+    out = warp_sum(out);
+  }
+  if (lane == 0) {
+    a.out[t] = out;
+    a.lse[t] = __fadd_rn(__fmul_rn(m, a.scale), ls);
   }
 }
 
@@ -280,27 +316,43 @@ __global__ void __launch_bounds__(1024) combine_kernel(const CombineArgs a) {
 __global__ void __launch_bounds__(256)
     scatter_kernel(const float* dx, const int32_t* n_rows, const int32_t* map, int H,
                    int slices, int64_t slice_stride, __nv_bfloat16* grad_hidden) {
-  const int vecs = H / 8;
+  ptx::grid_dependents_launch();
+  ptx::grid_dependency_wait();
+  const int vecs = H / 4;
   const int64_t total = (int64_t)*n_rows * vecs;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t c = i / vecs;
-    const int v = (int)(i - c * vecs);
-    const float4* src = reinterpret_cast<const float4*>(dx + c * H + v * 8);
-    float4 x = src[0], y = src[1];
+    const int v = (int)(i - c * vecs) * 4;
+    const float* src = dx + c * H + v;
+    float4 x = *reinterpret_cast<const float4*>(src);
+#pragma unroll 4
     for (int k = 1; k < slices; ++k) {
-      src = reinterpret_cast<const float4*>(dx + k * slice_stride + c * H + v * 8);
-      const float4 x2 = src[0], y2 = src[1];
-      x.x += x2.x; x.y += x2.y; x.z += x2.z; x.w += x2.w;
-      y.x += y2.x; y.y += y2.y; y.z += y2.z; y.w += y2.w;
+      const float4 y = *reinterpret_cast<const float4*>(src + k * slice_stride);
+      x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
     }
-    __nv_bfloat162 b[4] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w),
-                           __floats2bfloat162_rn(y.x, y.y), __floats2bfloat162_rn(y.z, y.w)};
-    *reinterpret_cast<uint4*>(grad_hidden + (int64_t)map[c] * H + v * 8) =
-        *reinterpret_cast<uint4*>(b);
+    __nv_bfloat162 b[2] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w)};
+    *reinterpret_cast<uint2*>(grad_hidden + (int64_t)map[c] * H + v) = *reinterpret_cast<uint2*>(b);
   }
 }
 
 // ------------------------------------------------------------------- host --
+
+// Launches with programmatic stream serialization allowed: the kernels' first
+// statement waits for the grid before them.
+template <class... P, class... A>
+fp8rl_status launch(void (*kernel)(P...), int64_t grid, int threads, cudaStream_t stream,
+                    const char* what, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_check(cudaLaunchKernelEx(&cfg, kernel, P(args)...), what);
+}
 
 // The workspace's parts, in order, each 256-byte aligned.
 struct Plan {
@@ -434,10 +486,10 @@ fp8rl_status pack_rows(const Call& c, const Plan& pl, const DeviceState* ds, int
     int32_t* ids = reinterpret_cast<int32_t*>(ws + pl.ids);
     float* p = reinterpret_cast<float*>(ws + pl.p);
     float* lp = backward ? nullptr : reinterpret_cast<float*>(ws + pl.lp);
-    teacher_kernel<<<(unsigned)((rows + kTeacherWarps - 1) / kTeacherWarps), kTeacherWarps * 32, 0,
-                     c.stream>>>(c.ids + t0 * c.K, c.logits + t0 * c.K, rows, (int)c.K, (int)c.V,
-                                 c.scale, ids, p, lp, f, ds->status);
-    const fp8rl_status st = cuda_check(cudaGetLastError(), "teacher_kernel launch");
+    const fp8rl_status st =
+        launch(teacher_kernel, (rows + kTeacherWarps - 1) / kTeacherWarps, kTeacherWarps * 32,
+               c.stream, "teacher_kernel launch", c.ids + t0 * c.K, c.logits + t0 * c.K, rows,
+               (int)c.K, (int)c.V, c.scale, ids, p, lp, f, ds->status);
     if (st != FP8RL_OK) return st;
     flags = f;
     va->ids = ids;
@@ -448,7 +500,7 @@ fp8rl_status pack_rows(const Call& c, const Plan& pl, const DeviceState* ds, int
   r.T = rows;
   r.V = (int)c.V;
   r.H = (int)c.H;
-  r.rows_per_cta = (int)std::max<int64_t>(8, (rows + 4 * ds->sm_count - 1) / (4 * ds->sm_count));
+  r.rows_per_cta = (int)((rows + 4 * ds->sm_count - 1) / (4 * ds->sm_count));
   r.hidden = reinterpret_cast<const __nv_bfloat16*>(c.hidden) + t0 * c.ldh;
   r.ldh = c.ldh;
   r.x = reinterpret_cast<__nv_bfloat16*>(ws + pl.x);
@@ -467,7 +519,6 @@ fp8rl_status pack_rows(const Call& c, const Plan& pl, const DeviceState* ds, int
     r.out1 = c.lse_out + t0;
   }
   r.status = ds->status;
-  rows_kernel<<<(unsigned)((rows + r.rows_per_cta - 1) / r.rows_per_cta), kRowThreads, 0, c.stream>>>(r);
   va->x = r.x;
   va->w = reinterpret_cast<const __nv_bfloat16*>(c.weight);
   va->ldw = c.ldw;
@@ -481,7 +532,20 @@ fp8rl_status pack_rows(const Call& c, const Plan& pl, const DeviceState* ds, int
   va->tgt = r.tgt;
   va->K = (int)c.K;
   va->status = ds->status;
-  return cuda_check(cudaGetLastError(), "rows_kernel launch");
+  return launch(rows_kernel, (rows + r.rows_per_cta - 1) / r.rows_per_cta, kRowThreads, c.stream,
+                "rows_kernel launch", r);
+}
+
+// Few rows: one CTA a row, the row's parts across all threads.  Many: up to 16
+// rows a CTA, whose loads are whole 128-byte lines.
+fp8rl_status launch_combine(const CombineArgs& b, int64_t rows, const DeviceState* ds,
+                            cudaStream_t stream) {
+  const char* what = "combine_kernel launch";
+  if (rows <= 2 * ds->sm_count)
+    return launch(combine_kernel<1>, rows, kCombineThreads, stream, what, b);
+  if (rows <= 8 * ds->sm_count)
+    return launch(combine_kernel<4>, (rows + 3) / 4, kCombineThreads, stream, what, b);
+  return launch(combine_kernel<16>, (rows + 15) / 16, kCombineThreads, stream, what, b);
 }
 
 fp8rl_status run_forward(const Call& c) {
@@ -511,8 +575,7 @@ fp8rl_status run_forward(const Call& c) {
     b.scale = c.scale;
     b.out = c.out + t0;
     b.lse = c.lse_out + t0;
-    combine_kernel<<<(unsigned)((rows + 31) / 32), 1024, 0, c.stream>>>(b);
-    if ((st = cuda_check(cudaGetLastError(), "combine_kernel launch")) != FP8RL_OK) return st;
+    if ((st = launch_combine(b, rows, ds, c.stream)) != FP8RL_OK) return st;
   }
   return ok();
 }
@@ -541,11 +604,11 @@ fp8rl_status run_backward(const Call& c, float coef) {
   va.dw = reinterpret_cast<__nv_bfloat16*>(c.grad_weight);
   if ((st = vocab_backward(va, ds, c.stream)) != FP8RL_OK) return st;
   if (c.grad_hidden) {
-    const int64_t vecs = c.T * (c.H / 8);
-    scatter_kernel<<<(unsigned)std::min<int64_t>((vecs + 255) / 256, 8 * ds->sm_count), 256, 0,
-                     c.stream>>>(va.dx, va.n_rows, va.map, (int)c.H, va.slices, (int64_t)va.rows_pad * c.H,
-                                 reinterpret_cast<__nv_bfloat16*>(c.grad_hidden));
-    if ((st = cuda_check(cudaGetLastError(), "scatter_kernel launch")) != FP8RL_OK) return st;
+    const int64_t ctas = (c.T * (c.H / 4) + 255) / 256;
+    st = launch(scatter_kernel, std::min<int64_t>(ctas, 16 * ds->sm_count), 256, c.stream,
+                "scatter_kernel launch", va.dx, va.n_rows, va.map, (int)c.H, va.slices,
+                (int64_t)va.rows_pad * c.H, reinterpret_cast<__nv_bfloat16*>(c.grad_hidden));
+    if (st != FP8RL_OK) return st;
   }
   return ok();
 }

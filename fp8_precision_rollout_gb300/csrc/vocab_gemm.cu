@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     st->abort_flag = 0;
     mbar_fence_init();
   }
+  grid_dependents_launch();
   grid_dependency_wait();
   // both CTAs' barriers exist before either CTA's work refers to them
   __syncthreads();
