@@ -115,6 +115,7 @@ struct RowsArgs {
   float coef;                  // +-scale
   float* lse_c;
   float* gcoef_c;
+  int lo_off;                  // > 0: rows repeat from here on (T <= lo_off)
   __nv_bfloat16* grad_hidden;  // [T, H] rows of left-out tokens become 0, or null
   uint32_t* status;
 };
@@ -169,6 +170,13 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsArgs a) {
         a.lse_c[c] = a.lse[t];
         a.gcoef_c[c] = a.grad[t] * a.coef;
       }
+      if (a.lo_off) {
+        const int c2 = c + a.lo_off;
+        a.map[c2] = (int32_t)t;
+        a.tgt[c2] = f;
+        a.lse_c[c2] = a.lse[t];
+        a.gcoef_c[c2] = a.grad[t] * a.coef;
+      }
     } else if (t < r1 && a.out0) {
       a.out0[t] = 0.0f;
       a.out1[t] = 0.0f;
@@ -179,21 +187,39 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsArgs a) {
     for (int i = tid; i < here * vecs; i += kRowThreads) {
       const int r = i / vecs, v = i - r * vecs;
       const int dst = idx[r];
-      if (dst >= 0)
-        reinterpret_cast<uint4*>(a.x + (int64_t)dst * a.H)[v] =
-            __ldg(reinterpret_cast<const uint4*>(a.hidden + (c0 + r) * a.ldh) + v);
-      else if (a.grad_hidden)
+      if (dst >= 0) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.hidden + (c0 + r) * a.ldh) + v);
+        reinterpret_cast<uint4*>(a.x + (int64_t)dst * a.H)[v] = x;
+        if (a.lo_off) reinterpret_cast<uint4*>(a.x + (int64_t)(dst + a.lo_off) * a.H)[v] = x;
+      } else if (a.grad_hidden)
         reinterpret_cast<uint4*>(a.grad_hidden + (c0 + r) * a.H)[v] = make_uint4(0, 0, 0, 0);
     }
     __syncthreads();
   }
   if (r1 == a.T) {
-    if (tid == 0) *a.n_rows = base;
+    // n_rows[0]: rows of the products; n_rows[1]: kept tokens
+    const int last = base && a.lo_off ? a.lo_off + base : base;
+    if (tid == 0) {
+      a.n_rows[0] = last;
+      a.n_rows[1] = base;
+    }
     if (a.grad) {
-      // dW sums over rows in steps of 64: the rows that fill the last step are zero
-      const int end = (max(base, 1) + 63) / 64 * 64;
-      uint4* to = reinterpret_cast<uint4*>(a.x + (int64_t)base * a.H);
-      for (int64_t v = tid; v < (int64_t)(end - base) * vecs; v += kRowThreads)
+      // dW sums over rows in steps of 64: the rows between the two copies and
+      // those that fill the last step are zero
+      if (base && a.lo_off) {
+        for (int c = base + tid; c < a.lo_off; c += kRowThreads) {
+          a.map[c] = 0;
+          a.tgt[c] = -1;
+          a.lse_c[c] = 0.0f;
+          a.gcoef_c[c] = 0.0f;
+        }
+        uint4* to = reinterpret_cast<uint4*>(a.x + (int64_t)base * a.H);
+        for (int64_t v = tid; v < (int64_t)(a.lo_off - base) * vecs; v += kRowThreads)
+          to[v] = make_uint4(0, 0, 0, 0);
+      }
+      const int end = (max(last, 1) + 63) / 64 * 64;
+      uint4* to = reinterpret_cast<uint4*>(a.x + (int64_t)last * a.H);
+      for (int64_t v = tid; v < (int64_t)(end - last) * vecs; v += kRowThreads)
         to[v] = make_uint4(0, 0, 0, 0);
     }
   }
@@ -211,20 +237,6 @@ struct CombineArgs {
   float* out;   // logp or loss, [T]
   float* lse;   // [T]
 };
-
-// Softmax partials (m, r): a maximum and the sum of the exponentials relative
-// to it less the maximum's own 1.  Nothing: (-inf, -1).  join adds (m2, r2).
-__device__ __forceinline__ void join(float& m, float& r, float m2, float r2, float k2) {
-  const float d = (m2 - m) * k2;
-  if (m2 > m) {
-    r = r2 + (1.0f + r) * exp2f(-d);
-    m = m2;
-  } else if (m2 == -INFINITY) {
-    r += 1.0f + r2;               // adds nothing, or a NaN
-  } else {
-    r = r + (1.0f + r2) * exp2f(d);
-  }
-}
 
 constexpr int kCombineThreads = 1024, kCombineBatch = 8;
 
@@ -258,8 +270,8 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
 #pragma unroll
       for (int o = kCombineBatch / 2; o; o >>= 1)
 #pragma unroll
-        for (int b = 0; b < o; ++b) join(q[b].x, q[b].y, q[b + o].x, q[b + o].y, k2);
-      join(m, r, q[0].x, q[0].y, k2);
+        for (int b = 0; b < o; ++b) vocab_join(q[b].x, q[b].y, q[b + o].x, q[b + o].y, k2);
+      vocab_join(m, r, q[0].x, q[0].y, k2);
     }
   }
 #pragma unroll
@@ -267,7 +279,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
     const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, o), r2 = __shfl_xor_sync(0xFFFFFFFFu, r, o);
     // both lanes join (lower, higher), so that both hold the same bits
     float ml = (lane & o) ? m2 : m, rl = (lane & o) ? r2 : r;
-    join(ml, rl, (lane & o) ? m : m2, (lane & o) ? r : r2, k2);
+    vocab_join(ml, rl, (lane & o) ? m : m2, (lane & o) ? r : r2, k2);
     m = ml;
     r = rl;
   }
@@ -284,7 +296,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
   for (int o = 1; o < 32; o <<= 1) {
     const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, o), r2 = __shfl_xor_sync(0xFFFFFFFFu, r, o);
     float ml = (lane & o) ? m2 : m, rl = (lane & o) ? r2 : r;
-    join(ml, rl, (lane & o) ? m : m2, (lane & o) ? r : r2, k2);
+    vocab_join(ml, rl, (lane & o) ? m : m2, (lane & o) ? r : r2, k2);
     m = ml;
     r = rl;
   }
@@ -311,27 +323,49 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
   }
 }
 
-// dX of the packed rows (FP32, the slices' sums added in order) -> grad_hidden
-// rows of their tokens.
+// dX of the packed rows (FP32, the slices' sums and a row's two copies added in
+// a fixed order) -> grad_hidden rows of their tokens.  kG lane groups of a
+// warp share the slices of 32 / kG consecutive float4: with 32 slices and few
+// rows one thread's chain of loads would be the kernel's time.
+template <int kG>
 __global__ void __launch_bounds__(256)
     scatter_kernel(const float* dx, const int32_t* n_rows, const int32_t* map, int H,
-                   int slices, int64_t slice_stride, __nv_bfloat16* grad_hidden) {
+                   int slices, int64_t slice_stride, int lo_off, __nv_bfloat16* grad_hidden) {
   ptx::grid_dependents_launch();
   ptx::grid_dependency_wait();
+  constexpr int kW = 32 / kG;
   const int vecs = H / 4;
-  const int64_t total = (int64_t)*n_rows * vecs;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+  const int lane = threadIdx.x & 31, group = lane / kW;
+  const int64_t total = (int64_t)n_rows[1] * vecs;
+  const int64_t warp = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), warps = (int64_t)gridDim.x * 8;
+  for (int64_t i0 = warp * kW; i0 < total; i0 += warps * kW) {
+    const int64_t i = i0 + lane % kW;
     const int64_t c = i / vecs;
     const int v = (int)(i - c * vecs) * 4;
-    const float* src = dx + c * H + v;
-    float4 x = *reinterpret_cast<const float4*>(src);
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (i < total) {
+      const float* src = dx + c * H + v;
 #pragma unroll 4
-    for (int k = 1; k < slices; ++k) {
-      const float4 y = *reinterpret_cast<const float4*>(src + k * slice_stride);
-      x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+      for (int k = group; k < slices; k += kG) {
+        const float4 y = *reinterpret_cast<const float4*>(src + k * slice_stride);
+        x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+        if (lo_off) {
+          const float4 z = *reinterpret_cast<const float4*>(src + k * slice_stride + (int64_t)lo_off * H);
+          x.x += z.x; x.y += z.y; x.z += z.z; x.w += z.w;
+        }
+      }
     }
-    __nv_bfloat162 b[2] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w)};
-    *reinterpret_cast<uint2*>(grad_hidden + (int64_t)map[c] * H + v) = *reinterpret_cast<uint2*>(b);
+#pragma unroll
+    for (int o = kW; o < 32; o <<= 1) {
+      x.x += __shfl_xor_sync(0xFFFFFFFFu, x.x, o);
+      x.y += __shfl_xor_sync(0xFFFFFFFFu, x.y, o);
+      x.z += __shfl_xor_sync(0xFFFFFFFFu, x.z, o);
+      x.w += __shfl_xor_sync(0xFFFFFFFFu, x.w, o);
+    }
+    if (i < total && group == 0) {
+      __nv_bfloat162 b[2] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w)};
+      *reinterpret_cast<uint2*>(grad_hidden + (int64_t)map[c] * H + v) = *reinterpret_cast<uint2*>(b);
+    }
   }
 }
 
@@ -365,6 +399,14 @@ struct Plan {
 
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
+// Rounding G to BF16 is averaged out where many tokens add up, but with few it
+// is the gradients' largest error.  Up to 128 tokens G's rows are therefore
+// kept twice, rounded and what the rounding lost, in rows that the tiles (256
+// rows) have anyway: from 32, 64 or 128 on, so that dW sums 64 rows at least.
+int lo_offset(int64_t tokens) {
+  return tokens > 128 ? 0 : (tokens > 64 ? 128 : (tokens > 32 ? 64 : 32));
+}
+
 // Forward: tokens go in pieces whose softmax partials fit kPartBytes, so the
 // workspace grows with neither tokens x vocab nor tokens beyond a piece.
 // Backward: the vocabulary goes in pieces whose G fits kGradBytes.
@@ -373,11 +415,12 @@ constexpr int64_t kGradBytes = 192ll << 20;   // each of two buffers
 
 Plan make_plan(int64_t T, int64_t H, int64_t V, int64_t K, bool backward) {
   Plan pl;
-  const int64_t parts = (V + kVocabPart - 1) / kVocabPart;
   pl.rows = T;
+  int64_t parts = 0;
   if (!backward) {
-    const int64_t most = std::max<int64_t>(2048, kPartBytes / (parts * 8) / kVocabPad * kVocabPad);
-    pl.rows = std::min(T, most);
+    const int64_t most = kPartBytes / (vocab_most_parts(T, V) * 8) / kVocabPad * kVocabPad;
+    pl.rows = std::min(T, std::max<int64_t>(2048, most));
+    parts = vocab_most_parts(pl.rows, V);
   }
   pl.rows_pad = round_up(std::max<int64_t>(pl.rows, 1), kVocabPad);
   size_t at = 0;
@@ -513,6 +556,7 @@ fp8rl_status pack_rows(const Call& c, const Plan& pl, const DeviceState* ds, int
     r.coef = coef;
     r.lse_c = reinterpret_cast<float*>(ws + pl.lse);
     r.gcoef_c = reinterpret_cast<float*>(ws + pl.gcoef);
+    r.lo_off = va->lo_off = lo_offset(rows);
     r.grad_hidden = reinterpret_cast<__nv_bfloat16*>(c.grad_hidden);
   } else {
     r.out0 = c.out + t0;
@@ -566,7 +610,7 @@ fp8rl_status run_forward(const Call& c) {
     b.n_rows = va.n_rows;
     b.map = va.map;
     b.part = va.part;
-    b.parts = (int)((c.V + kVocabPart - 1) / kVocabPart);
+    b.parts = vocab_parts(va, ds);
     b.rows_pad = va.rows_pad;
     b.K = va.K;
     b.zt = va.zt;
@@ -604,10 +648,13 @@ fp8rl_status run_backward(const Call& c, float coef) {
   va.dw = reinterpret_cast<__nv_bfloat16*>(c.grad_weight);
   if ((st = vocab_backward(va, ds, c.stream)) != FP8RL_OK) return st;
   if (c.grad_hidden) {
-    const int64_t ctas = (c.T * (c.H / 4) + 255) / 256;
-    st = launch(scatter_kernel, std::min<int64_t>(ctas, 16 * ds->sm_count), 256, c.stream,
-                "scatter_kernel launch", va.dx, va.n_rows, va.map, (int)c.H, va.slices,
-                (int64_t)va.rows_pad * c.H, reinterpret_cast<__nv_bfloat16*>(c.grad_hidden));
+    const bool shared = va.slices >= 8;
+    const int64_t per_cta = shared ? 32 : 256;
+    const int64_t ctas = (c.T * (c.H / 4) + per_cta - 1) / per_cta;
+    st = launch(shared ? scatter_kernel<8> : scatter_kernel<1>,
+                std::min<int64_t>(ctas, 16 * ds->sm_count), 256, c.stream, "scatter_kernel launch",
+                va.dx, va.n_rows, va.map, (int)c.H, va.slices, (int64_t)va.rows_pad * c.H,
+                va.lo_off, reinterpret_cast<__nv_bfloat16*>(c.grad_hidden));
     if (st != FP8RL_OK) return st;
   }
   return ok();

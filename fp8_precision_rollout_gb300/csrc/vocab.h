@@ -11,8 +11,6 @@
 
 namespace fp8rl {
 
-// Columns of the vocabulary that one softmax partial covers.
-constexpr int kVocabPart = 128;
 // Row counts, and pieces of the vocabulary, are padded to this in the
 // workspace: the tile's rows and columns.
 constexpr int kVocabPad = 256;
@@ -28,6 +26,8 @@ struct VocabArgs {
   int rows_cap, rows_pad;
   const int32_t* n_rows;
   const int32_t* map;       // [rows_pad] token of each packed row
+  int lo_off;               // backward: rows from here on repeat the rows from 0
+                            // on and hold what rounding G to BF16 lost (0: none)
   float scale;              // logits = scale * x w^T
   // sparse target distribution: K = 0, one target tgt[c] of probability 1;
   // K > 0, entries ids/p[map[c] * K + j], ids ascending, absent ones INT_MAX
@@ -38,7 +38,7 @@ struct VocabArgs {
   // forward: per (column part, row) the maximum of x w^T and the sum of
   // exp(scale * (x w^T - maximum)) less 1, the maximum's own term ((-inf, -1)
   // for nothing); the entries' x w^T ([row] or [row, K])
-  float2* part;             // [ceil(V / kVocabPart), rows_pad]
+  float2* part;             // [parts, rows_pad]; see vocab_parts
   float* zt;
   // backward: log-sum-exp and signed, scaled upstream gradient of each row;
   // G = gcoef * (softmax - target distribution)
@@ -52,11 +52,41 @@ struct VocabArgs {
   uint32_t* status;
 };
 
+// Softmax partials per row that vocab_forward writes, and an upper bound for
+// calls of rows_pad rows that needs no device.
+int vocab_parts(const VocabArgs& a, const DeviceState* ds);
+int64_t vocab_most_parts(int64_t rows, int64_t V);
+constexpr int kMostSms = 512;   // of any GPU the library runs on
 // Softmax partials and target logits of every row over the whole vocabulary.
 fp8rl_status vocab_forward(const VocabArgs& a, const DeviceState* ds, cudaStream_t stream);
 // G, dx (per slice) and dw over the whole vocabulary, piece by piece.
 fp8rl_status vocab_backward(const VocabArgs& a, const DeviceState* ds, cudaStream_t stream);
 // Slices that give the dX product of `rows` x H enough tiles to fill the GPU.
 int vocab_dx_slices(int64_t rows, int64_t H, int64_t vc);
+
+// The same for up to kVocabFew rows whose hidden states fit in shared memory
+// as FP32 (vocab_few.cu): a read of the weights by plain FP32 arithmetic.
+constexpr int kVocabFew = 8;
+constexpr int kVocabFewBytes = 192 << 10;
+inline int vocab_few_rows(int rows) { return rows <= 2 ? rows : (rows <= 4 ? 4 : 8); }
+inline bool vocab_few(int rows, int64_t H) {
+  return rows <= kVocabFew && vocab_few_rows(rows) * H * 4 <= kVocabFewBytes;
+}
+fp8rl_status vocab_forward_few(const VocabArgs& a, const DeviceState* ds, cudaStream_t stream);
+
+// Softmax partials (m, r): a maximum and the sum of the exponentials relative
+// to it less the maximum's own 1.  Nothing: (-inf, -1).  Joins (m2, r2) into
+// (m, r); k2 = scale * log2 e.
+__device__ __forceinline__ void vocab_join(float& m, float& r, float m2, float r2, float k2) {
+  const float d = (m2 - m) * k2;
+  if (m2 > m) {
+    r = r2 + (1.0f + r) * exp2f(-d);
+    m = m2;
+  } else if (m2 == -INFINITY) {
+    r += 1.0f + r2;               // adds nothing, or a NaN
+  } else {
+    r = r + (1.0f + r2) * exp2f(d);
+  }
+}
 
 }  // namespace fp8rl

@@ -57,9 +57,9 @@ constexpr int kRun = 8;
 enum Kind { kStats = 0, kGrad = 1, kDx = 2, kDw = 3 };
 
 // kind::f16: D = F32 (bits 4-5 = 1), A = B = BF16 (bits 7-9, 10-12 = 1),
-// MN-major A and B (bits 15, 16), N >> 3 in bits 17-22, M >> 4 in bits 24-28.
-constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kTile >> 3) << 17) |
-                            ((uint32_t)(kTile >> 4) << 24);
+// MN-major A and B (bits 15, 16), N >> 3 in bits 17-22 (set per job), M >> 4 in
+// bits 24-28.
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kTile >> 4) << 24);
 constexpr uint32_t kMnA = 1u << 15, kMnB = 1u << 16;
 
 template <bool kFwd>
@@ -89,8 +89,10 @@ struct Params {
   CUtensorMap g_k, w_mn, dx_out;    // dX
   CUtensorMap g_mn, x_mn, dw_out;   // dW
   VocabArgs a;
+  int tn;          // stats, grad: columns of a tile, a multiple of 32 up to kTile
   int v_grad;      // first vocabulary column of the grad piece
   int n_grad;      // its column tiles (0: none)
+  __nv_bfloat16* g_row;   // the piece of G written
   int v_prod;      // first column of the piece whose products are formed
   int vc_prod;     // its columns
   int dx_tiles_n;  // column tiles of H when dX / dW are wanted, else 0
@@ -123,7 +125,7 @@ __device__ __forceinline__ Schedule make_schedule(const Params& p, int n, int c,
   s.np = np;
   s.mt = (max(n, kFwd ? 0 : 1) + kTile - 1) / kTile;
   if (kFwd) {
-    s.nstats = s.mt * ((p.a.V + kTile - 1) / kTile);
+    s.nstats = s.mt * ((p.a.V + p.tn - 1) / p.tn);
     return s;
   }
   // dX jobs sum over a whole slice and are the longest: they go first, dealt
@@ -162,8 +164,8 @@ __device__ __forceinline__ bool get_job(const Params& p, const Schedule& s, int 
     const int t = s.c + i * s.np;
     if (t >= s.nstats) return false;
     int m, nn;
-    band_tile(t, s.mt, (p.a.V + kTile - 1) / kTile, &m, &nn);
-    *j = {kStats, h_steps, m * kTile, nn * kTile, 0, 0};
+    band_tile(t, s.mt, (p.a.V + p.tn - 1) / p.tn, &m, &nn);
+    *j = {kStats, h_steps, m * kTile, nn * p.tn, 0, 0};
     return true;
   }
   const int mine = s.per + (s.c < s.rem ? 1 : 0);
@@ -191,7 +193,7 @@ __device__ __forceinline__ bool get_job(const Params& p, const Schedule& s, int 
   } else {
     int m, nn;
     band_tile(t - s.ndw, s.mt, p.n_grad, &m, &nn);
-    *j = {kGrad, h_steps, m * kTile, nn * kTile, 0, 0};
+    *j = {kGrad, h_steps, m * kTile, nn * p.tn, 0, 0};
   }
   return true;
 }
@@ -262,12 +264,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             break;
           }
           const uint32_t fb = mapa(smem_u32(&st->full[s]), 0);
-          if (rank == 0) mbar_expect_tx(smem_u32(&st->full[s]), 2 * kStageBytes);
+          const bool head = kFwd || j.kind == kGrad;
+          // (a narrower head tile loads fewer rows of W)
+          if (rank == 0)
+            mbar_expect_tx(smem_u32(&st->full[s]), head ? 2 * kOperand + p.tn * kBK * 2 : 2 * kStageBytes);
           const uint32_t da = s_base + s * kStageBytes, db = da + kOperand;
           const int kk = j.k0 + k * kBK;
-          if (kFwd || j.kind == kGrad) {
+          if (head) {
             tma_load_2d_pair(da, &p.x_k, fb, kk, j.a0 + half);
-            tma_load_2d_pair(db, &p.w_k, fb, kk, (kFwd ? 0 : p.v_grad) + j.b0 + half);
+            tma_load_2d_pair(db, &p.w_k, fb, kk, (kFwd ? 0 : p.v_grad) + j.b0 + (int)rank * (p.tn / 2));
           } else if (j.kind == kDx) {
             tma_load_2d_pair(da, &p.g_k, fb, kk, j.a0 + half);
             tma_load_2d_pair(db, &p.w_mn, fb, j.b0 + half, p.v_prod + kk);
@@ -301,7 +306,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       for (int i = 0; alive && get_job<kFwd>(p, sch, n, i, &j); ++i) {
         const bool a_mn = !kFwd && j.kind == kDw;
         const bool b_mn = !kFwd && j.kind >= kDx;
-        const uint32_t id = kIdesc | (a_mn ? kMnA : 0u) | (b_mn ? kMnB : 0u);
+        const int cols = (kFwd || j.kind == kGrad) ? p.tn : kTile;
+        const uint32_t id =
+            kIdesc | ((uint32_t)(cols >> 3) << 17) | (a_mn ? kMnA : 0u) | (b_mn ? kMnB : 0u);
         for (int k = 0; k < j.steps; ++k, ++it) {
           const bool fresh = k == 0 || (kFwd && k % kRun == 0);
           const bool last = k + 1 == j.steps || (kFwd && (k + 1) % kRun == 0);
@@ -336,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // ----------------------------------------------------------- epilogue --
     const int q = warp & 3;                  // TMEM lane quarter of this warp
     const int h = (warp - 2) >> 2;           // column half
-    const uint32_t tm = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * 128);
+    const uint32_t tmq = tmem_base + ((uint32_t)(q * 32) << 16);
     const uint32_t te[2] = {mapa(smem_u32(&st->tempty[0]), 0), mapa(smem_u32(&st->tempty[1]), 0)};
     const uint32_t stg = out_base + (uint32_t)((warp - 2) * kStageOutBytes);
     const float k2 = a.scale * kLog2e;
@@ -346,13 +353,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     for (int i = 0; alive && get_job<kFwd>(p, sch, n, i, &j); ++i) {
       const int row0 = j.a0 + (int)rank * 128 + q * 32;
       const int row = row0 + lane;
-      const int col0 = j.b0 + h * 128;       // first column of this half
+      // this half of the tile: columns [col0, col0 + hw)
+      const int hw = (kFwd || j.kind == kGrad) ? p.tn / 2 : kTile / 2;
+      const int col0 = j.b0 + h * hw;
+      const uint32_t tm = tmq + (uint32_t)(h * hw);
       if constexpr (kFwd) {
         // Runs of kRun steps are summed on the tensor cores and the runs added
         // here, rounded to nearest: the tensor cores truncate every addition,
         // a bias that grows with the length of the run.
         const bool ok = row < n;
-        const int32_t tgt = (ok && a.K == 0) ? a.tgt[row] - col0 : -1;
+        const int32_t tgt = (ok && a.K == 0) ? a.tgt[row] - col0 : -1;   // in [0, hw) if here
         const int32_t* ids = nullptr;
         int cur = 0;
         if (ok && a.K) {
@@ -390,10 +400,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
         if (!alive) break;
         if (col0 < a.V) {
-          if (col0 + 128 > a.V) {
+          const int live = min(hw, a.V - col0);
+          if (live < 128) {
 #pragma unroll
             for (int e = 0; e < 128; ++e)
-              if (col0 + e >= a.V) acc[e] = -INFINITY;
+              if (e >= live) acc[e] = -INFINITY;
           }
           float mx = -INFINITY;
 #pragma unroll
@@ -409,17 +420,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             if (acc[e + 1] == mx) ties += 1.0f; else s1 += e1;
           }
           const float rest = mx == -INFINITY ? s0 + s1 - 1.0f : s0 + s1 + (ties - 1.0f);
-          if (ok) a.part[(int64_t)(col0 / kVocabPart) * a.rows_pad + row] = make_float2(mx, rest);
-          if (__any_sync(0xFFFFFFFFu, tgt >= 0 && tgt < 128)) {
+          if (ok) a.part[(int64_t)(col0 / hw) * a.rows_pad + row] = make_float2(mx, rest);
+          if (__any_sync(0xFFFFFFFFu, tgt >= 0 && tgt < hw)) {
             float z = 0.0f;
 #pragma unroll
             for (int e = 0; e < 128; ++e) z = tgt == e ? acc[e] : z;
-            if (tgt >= 0 && tgt < 128) a.zt[row] = z;
+            if (tgt >= 0 && tgt < hw) a.zt[row] = z;
           }
           if (ids) {
             for (; cur < a.K; ++cur) {
               const int32_t rel = __ldg(ids + cur) - col0;
-              if (rel >= 128) break;
+              if (rel >= hw) break;
               float z = 0.0f;
 #pragma unroll
               for (int e = 0; e < 128; ++e) z = rel == e ? acc[e] : z;
@@ -471,6 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(te[buf]);
           }
+          if ((kFwd || j.kind == kGrad) && c * 32 >= hw) continue;
           if (j.kind == kDx) {
             // FP32 boxes of 32 columns; two in flight
             const uint32_t box = stg + (c & 1) * kBoxBytes;
@@ -486,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             __syncwarp();
             if (lane == 0) {
               const int col = col0 + c * 32;
-              if (col < a.H) {
+              if (col < a.H && row0 < n) {   // rows past n hold nothing
                 const int r = j.slice * a.rows_pad + row0;
                 if (p.dx_first)
                   tma_store_2d(&p.dx_out, box, col, r);
@@ -520,9 +532,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
               const int live = ok ? a.V - (vcol + c * 32) : 0;   // columns that exist
 #pragma unroll
               for (int e = 0; e < 32; ++e) f[e] = e < live ? gc * f[e] : 0.0f;
+              if (a.lo_off && row >= a.lo_off) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) f[e] -= __bfloat162float(__float2bfloat16_rn(f[e]));
+              }
             }
-            // BF16 boxes of 64 columns
+            // BF16 boxes of 64 columns; a narrow G tile, whose halves are no whole
+            // boxes, is stored from the registers
             const uint32_t box = stg + (c >> 1) * kBoxBytes;
+            const bool direct = j.kind == kGrad && hw != kTile / 2;
+            __nv_bfloat16* grow = p.g_row + (int64_t)row * a.vc + col0 + c * 32;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               __nv_bfloat162 b0 = __floats2bfloat162_rn(f[e * 8], f[e * 8 + 1]);
@@ -530,11 +549,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
               __nv_bfloat162 b2 = __floats2bfloat162_rn(f[e * 8 + 4], f[e * 8 + 5]);
               __nv_bfloat162 b3 = __floats2bfloat162_rn(f[e * 8 + 6], f[e * 8 + 7]);
               const int chunk = (c & 1) * 4 + e;
+              if (direct) {
+                uint4 o = {*reinterpret_cast<uint32_t*>(&b0), *reinterpret_cast<uint32_t*>(&b1),
+                           *reinterpret_cast<uint32_t*>(&b2), *reinterpret_cast<uint32_t*>(&b3)};
+                if (c * 32 + e * 8 < hw && col0 + c * 32 + e * 8 < a.vc)
+                  *reinterpret_cast<uint4*>(grow + e * 8) = o;
+                continue;
+              }
               st_shared_v4(box + (uint32_t)(lane * 128 + ((chunk ^ (lane & 7)) * 16)),
                            *reinterpret_cast<uint32_t*>(&b0), *reinterpret_cast<uint32_t*>(&b1),
                            *reinterpret_cast<uint32_t*>(&b2), *reinterpret_cast<uint32_t*>(&b3));
             }
-            if (c & 1) {
+            if (!direct && (c & 1)) {
               fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) {
@@ -641,21 +667,74 @@ int vocab_dx_slices(int64_t rows, int64_t H, int64_t vc) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(want, vc / (8 * kBK)));
 }
 
+namespace {
+
+// Columns of the head tiles (stats, grad) for `mt` row tiles x V columns on
+// `pairs` pairs of SMs: the width, a multiple of `unit` from 64 on, whose rounds
+// take the least time, a round counted as its width plus 16 columns' worth of
+// overhead.  With many rounds that is the full width (and nothing else is
+// looked at from kNarrowTiles tiles on); with few, a narrower tile keeps the
+// last round from leaving most SMs idle: 32768 columns are 128 full tiles, two
+// rounds on 76 pairs, or two rounds of 224.
+constexpr int kNarrowTiles = 600, kNarrowest = 64;
+
+int head_tile(int64_t mt, int64_t V, int pairs, int unit) {
+  if (mt * tiles(V) > kNarrowTiles) return kTile;
+  int best = kTile;
+  int64_t cost = INT64_MAX;
+  for (int tn = kTile; tn >= kNarrowest; tn -= unit) {
+    const int64_t rounds = (mt * ((V + tn - 1) / tn) + pairs - 1) / pairs;
+    const int64_t c = rounds * (tn + 16);
+    if (c < cost) {
+      cost = c;
+      best = tn;
+    }
+  }
+  return best;
+}
+
+}  // namespace
+
+int vocab_parts(const VocabArgs& a, const DeviceState* ds) {
+  if (vocab_few(a.rows_cap, a.H)) return ds->sm_count;
+  int pairs = 1;
+  pairs_of<true>(ds, &pairs);
+  const int half = head_tile(a.rows_pad / kTile, a.V, pairs, 32) / 2;
+  return (a.V + half - 1) / half;
+}
+
+int64_t vocab_most_parts(int64_t rows, int64_t V) {
+  const bool narrow = tiles(std::max<int64_t>(rows, 1)) * tiles(V) <= kNarrowTiles;
+  const int64_t half = (narrow ? kNarrowest : kTile) / 2;
+  return std::max<int64_t>((V + half - 1) / half, kMostSms);
+}
+
 fp8rl_status vocab_forward(const VocabArgs& a, const DeviceState* ds, cudaStream_t stream) {
+  if (vocab_few(a.rows_cap, a.H)) return vocab_forward_few(a, ds, stream);
   Params p = {};
   p.a = a;
-  fp8rl_status st;
+  int pairs = 0;
+  fp8rl_status st = pairs_of<true>(ds, &pairs);
+  if (st != FP8RL_OK) return st;
+  p.tn = head_tile(a.rows_pad / kTile, a.V, pairs, 32);
   if ((st = map_bf16(&p.x_k, a.x, a.H, a.rows_pad, a.H, 128, "hidden")) != FP8RL_OK) return st;
-  if ((st = map_bf16(&p.w_k, a.w, a.H, a.V, a.ldw, 128, "weight")) != FP8RL_OK) return st;
-  return launch<true>(p, tiles(a.rows_cap) * tiles(a.V), ds, stream);
+  if ((st = map_bf16(&p.w_k, a.w, a.H, a.V, a.ldw, p.tn / 2, "weight")) != FP8RL_OK) return st;
+  return launch<true>(p, tiles(a.rows_cap) * ((a.V + p.tn - 1) / p.tn), ds, stream);
 }
 
 fp8rl_status vocab_backward(const VocabArgs& a, const DeviceState* ds, cudaStream_t stream) {
   Params p = {};
   p.a = a;
   fp8rl_status st;
+  // launch i: G of piece i, dX and dW of piece i - 1
+  const int64_t pieces = (a.V + a.vc - 1) / a.vc;
+  const int64_t mt = tiles(a.rows_pad), ht = tiles(a.H);
+  int pairs = 0;
+  if ((st = pairs_of<false>(ds, &pairs)) != FP8RL_OK) return st;
+  // (multiples of 64, so that G's columns are written to the end of dX's last step)
+  p.tn = pieces == 1 ? head_tile(mt, a.V, pairs, 64) : kTile;
   if ((st = map_bf16(&p.x_k, a.x, a.H, a.rows_pad, a.H, 128, "hidden")) != FP8RL_OK) return st;
-  if ((st = map_bf16(&p.w_k, a.w, a.H, a.V, a.ldw, 128, "weight")) != FP8RL_OK) return st;
+  if ((st = map_bf16(&p.w_k, a.w, a.H, a.V, a.ldw, p.tn / 2, "weight")) != FP8RL_OK) return st;
   if ((st = map_bf16(&p.x_mn, a.x, a.H, a.rows_pad, a.H, 64, "hidden")) != FP8RL_OK) return st;
   if ((st = map_bf16(&p.w_mn, a.w, a.H, a.V, a.ldw, 64, "weight")) != FP8RL_OK) return st;
   CUtensorMap g_out[2], g_k[2], g_mn[2];
@@ -678,16 +757,14 @@ fp8rl_status vocab_backward(const VocabArgs& a, const DeviceState* ds, cudaStrea
   } else {
     p.dw_out = p.x_k;
   }
-  // launch i: G of piece i, dX and dW of piece i - 1
-  const int64_t pieces = (a.V + a.vc - 1) / a.vc;
-  const int64_t mt = tiles(a.rows_cap), ht = tiles(a.H);
   for (int64_t i = 0; i <= pieces; ++i) {
     int64_t jobs = 0;
     p.n_grad = p.dx_tiles_n = p.dw_tiles_n = 0;
     p.vc_prod = 0;
     if (i < pieces) {
       p.v_grad = (int)(i * a.vc);
-      p.n_grad = (int)tiles(std::min<int64_t>(a.vc, a.V - p.v_grad));
+      p.n_grad = (int)((std::min<int64_t>(a.vc, a.V - p.v_grad) + p.tn - 1) / p.tn);
+      p.g_row = a.g[i & 1];
       p.g_out = g_out[i & 1];
       jobs += mt * p.n_grad;
     }
