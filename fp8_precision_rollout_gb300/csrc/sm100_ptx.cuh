@@ -11,6 +11,17 @@
 namespace fp8rl {
 namespace ptx {
 
+// True in one lane of the warp (all lanes must be converged here).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Every wait on an mbarrier gives up after this long; the kernel then records
 // the timeout in the library's device status word and returns.
 constexpr uint64_t kWaitLimitNs = 1000000000ull;

@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = st->tmem_base;
-  const int n = *a.n_rows;
+  const int n = __shfl_sync(0xFFFFFFFFu, *a.n_rows, 0);   // warp-uniform to the compiler too
   const Schedule sch = make_schedule<kFwd>(p, n, (int)(blockIdx.x >> 1), (int)(gridDim.x >> 1));
 
   if (warp == 0) {
@@ -299,7 +299,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     __syncwarp();
   } else if (warp == 1) {
     // --------------------------------------------------------- MMA issuer --
-    if (lane == 0 && rank == 0) {
+    // The whole warp walks the jobs, one elected lane issues: with uniform
+    // control flow the descriptors stay in uniform registers.
+    if (rank == 0) {
       uint32_t it = 0, use = 0;      // steps; uses of a TMEM buffer
       bool alive = true;
       Job j;
@@ -309,6 +311,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int cols = (kFwd || j.kind == kGrad) ? p.tn : kTile;
         const uint32_t id =
             kIdesc | ((uint32_t)(cols >> 3) << 17) | (a_mn ? kMnA : 0u) | (b_mn ? kMnB : 0u);
+        // 16 deep: 32 bytes along a K-major row, 16 rows of an MN-major block
+        const uint64_t da0 = a_mn ? sw128_desc_mn(s_base, kOperand / 2) : sw128_desc(s_base);
+        const uint64_t db0 = b_mn ? sw128_desc_mn(s_base + kOperand, kOperand / 2) : sw128_desc(s_base + kOperand);
+        const uint32_t qa = (a_mn ? 2048u : 32u) >> 4, qb = (b_mn ? 2048u : 32u) >> 4;
         for (int k = 0; k < j.steps; ++k, ++it) {
           const bool fresh = k == 0 || (kFwd && k % kRun == 0);
           const bool last = k + 1 == j.steps || (kFwd && (k + 1) % kRun == 0);
@@ -316,25 +322,22 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           const int s = it % STAGES;
           if ((fresh && !mbar_wait(smem_u32(&st->tempty[buf]), ((use >> 1) & 1u) ^ 1u, abort_flag,
                                    a.status, 52)) ||
-              !mbar_wait(smem_u32(&st->full[s]), (it / STAGES) & 1u, abort_flag, a.status, 53)) {
+              !mbar_wait(smem_u32(&st->full[s]), (it / STAGES) & 1u, abort_flag, a.status, 53))
             alive = false;
-            break;
-          }
+          alive = __all_sync(0xFFFFFFFFu, alive);
+          if (!alive) break;
           tc_fence_after();
-          const uint32_t d = tmem_base + buf * kTile;
-          const uint32_t sa = s_base + s * kStageBytes, sb = sa + kOperand;
+          if (elect_one()) {
+            const uint32_t d = tmem_base + buf * kTile;
+            const uint64_t da = da0 + (uint32_t)(s * (kStageBytes >> 4)), db = db0 + (uint32_t)(s * (kStageBytes >> 4));
 #pragma unroll
-          for (int q = 0; q < kBK / 16; ++q) {
-            // 16 deep: 32 bytes along a K-major row, 16 rows of an MN-major block
-            const uint64_t da = a_mn ? sw128_desc_mn(sa + q * 2048, kOperand / 2) : sw128_desc(sa + q * 32);
-            const uint64_t db = b_mn ? sw128_desc_mn(sb + q * 2048, kOperand / 2) : sw128_desc(sb + q * 32);
-            mma_f16_pair(d, da, db, id, (fresh && q == 0) ? 0u : 1u);
+            for (int q = 0; q < kBK / 16; ++q)
+              mma_f16_pair(d, da + q * qa, db + q * qb, id, (fresh && q == 0) ? 0u : 1u);
+            mma_commit_pair(smem_u32(&st->empty[s]));
+            if (last) mma_commit_pair(smem_u32(&st->tfull[buf]));
           }
-          mma_commit_pair(smem_u32(&st->empty[s]));
-          if (last) {
-            mma_commit_pair(smem_u32(&st->tfull[buf]));
-            ++use;
-          }
+          __syncwarp();
+          if (last) ++use;
         }
       }
     }
