@@ -58,8 +58,8 @@ __global__ void __launch_bounds__(kTeacherWarps * 32)
   __shared__ float su[kTeacherWarps][kMaxTopK];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t = (int64_t)blockIdx.x * kTeacherWarps + warp;
-  ptx::grid_dependents_launch();
   ptx::grid_dependency_wait();
+  ptx::grid_dependents_launch();
   if (t >= T) return;
   int32_t* id = sid[warp];
   float* u = su[warp];
@@ -128,8 +128,8 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsArgs a) {
   __shared__ int idx[kRowThreads];
   __shared__ int sbase;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  ptx::grid_dependents_launch();
   ptx::grid_dependency_wait();
+  ptx::grid_dependents_launch();
   const int64_t r0 = (int64_t)blockIdx.x * a.rows_per_cta;
   const int64_t r1 = min(a.T, r0 + a.rows_per_cta);
   int before = 0;
@@ -249,8 +249,8 @@ constexpr int kCombineThreads = 1024, kCombineBatch = 8;
 template <int R>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineArgs a) {
   __shared__ float sm[32][R], sr[32][R];
-  ptx::grid_dependents_launch();
   ptx::grid_dependency_wait();
+  ptx::grid_dependents_launch();
   const int n = *a.n_rows;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int c0 = blockIdx.x * R;
@@ -324,27 +324,49 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
 }
 
 // dX of the packed rows (FP32, the slices' sums and a row's two copies added in
-// a fixed order) -> grad_hidden rows of their tokens.  kG lane groups of a
-// warp share the slices of 32 / kG consecutive float4: with 32 slices and few
-// rows one thread's chain of loads would be the kernel's time.
-template <int kG>
+// a fixed order) -> grad_hidden rows of their tokens.  A read of dX and a write
+// of the gradient: 12.5 us for 3072 rows of 4096 in one slice.
 __global__ void __launch_bounds__(256)
-    scatter_kernel(const float* dx, const int32_t* n_rows, const int32_t* map, int H,
-                   int slices, int64_t slice_stride, int lo_off, __nv_bfloat16* grad_hidden) {
-  ptx::grid_dependents_launch();
+    scatter_kernel(const float* dx, const int32_t* n_rows, const int32_t* map, int H, int slices,
+                   int64_t slice_stride, __nv_bfloat16* grad_hidden) {
   ptx::grid_dependency_wait();
-  constexpr int kW = 32 / kG;
-  const int vecs = H / 4;
-  const int lane = threadIdx.x & 31, group = lane / kW;
+  ptx::grid_dependents_launch();
+  const int vecs = H / 8;
   const int64_t total = (int64_t)n_rows[1] * vecs;
-  const int64_t warp = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), warps = (int64_t)gridDim.x * 8;
-  for (int64_t i0 = warp * kW; i0 < total; i0 += warps * kW) {
-    const int64_t i = i0 + lane % kW;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t c = i / vecs;
-    const int v = (int)(i - c * vecs) * 4;
+    const int v = (int)(i - c * vecs) * 8;
+    const float4* src = reinterpret_cast<const float4*>(dx + c * H + v);
+    float4 x = src[0], y = src[1];
+#pragma unroll 4
+    for (int k = 1; k < slices; ++k) {
+      src = reinterpret_cast<const float4*>(dx + k * slice_stride + c * H + v);
+      const float4 x2 = src[0], y2 = src[1];
+      x.x += x2.x; x.y += x2.y; x.z += x2.z; x.w += x2.w;
+      y.x += y2.x; y.y += y2.y; y.z += y2.z; y.w += y2.w;
+    }
+    __nv_bfloat162 b[4] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w),
+                           __floats2bfloat162_rn(y.x, y.y), __floats2bfloat162_rn(y.z, y.w)};
+    *reinterpret_cast<uint4*>(grad_hidden + (int64_t)map[c] * H + v) = *reinterpret_cast<uint4*>(b);
+  }
+}
+
+// The same for few rows and many slices, where one thread's chain of loads
+// would be the kernel's time: the lane groups of a warp share the slices of 4
+// consecutive float4.  Grid: x = pieces of a row, y = rows (strided).
+__global__ void __launch_bounds__(256)
+    scatter_few_kernel(const float* dx, const int32_t* n_rows, const int32_t* map, int H,
+                       int slices, int64_t slice_stride, int lo_off, __nv_bfloat16* grad_hidden) {
+  ptx::grid_dependency_wait();
+  ptx::grid_dependents_launch();
+  constexpr int kG = 8, kW = 32 / kG;
+  const int lane = threadIdx.x & 31, group = lane / kW;
+  const int v = ((blockIdx.x * 8 + (threadIdx.x >> 5)) * kW + lane % kW) * 4;
+  const int n = n_rows[1];
+  for (int c = blockIdx.y; c < n; c += gridDim.y) {
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (i < total) {
-      const float* src = dx + c * H + v;
+    if (v < H) {
+      const float* src = dx + (int64_t)c * H + v;
 #pragma unroll 4
       for (int k = group; k < slices; k += kG) {
         const float4 y = *reinterpret_cast<const float4*>(src + k * slice_stride);
@@ -362,7 +384,7 @@ __global__ void __launch_bounds__(256)
       x.z += __shfl_xor_sync(0xFFFFFFFFu, x.z, o);
       x.w += __shfl_xor_sync(0xFFFFFFFFu, x.w, o);
     }
-    if (i < total && group == 0) {
+    if (v < H && group == 0) {
       __nv_bfloat162 b[2] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w)};
       *reinterpret_cast<uint2*>(grad_hidden + (int64_t)map[c] * H + v) = *reinterpret_cast<uint2*>(b);
     }
@@ -372,12 +394,12 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------- host --
 
 // Launches with programmatic stream serialization allowed: the kernels' first
-// statement waits for the grid before them.
+// statement waits for the grid before them, the second lets the next one start.
 template <class... P, class... A>
-fp8rl_status launch(void (*kernel)(P...), int64_t grid, int threads, cudaStream_t stream,
+fp8rl_status launch(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream,
                     const char* what, A... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -530,7 +552,7 @@ fp8rl_status pack_rows(const Call& c, const Plan& pl, const DeviceState* ds, int
     float* p = reinterpret_cast<float*>(ws + pl.p);
     float* lp = backward ? nullptr : reinterpret_cast<float*>(ws + pl.lp);
     const fp8rl_status st =
-        launch(teacher_kernel, (rows + kTeacherWarps - 1) / kTeacherWarps, kTeacherWarps * 32,
+        launch(teacher_kernel, dim3((unsigned)((rows + kTeacherWarps - 1) / kTeacherWarps)), kTeacherWarps * 32,
                c.stream, "teacher_kernel launch", c.ids + t0 * c.K, c.logits + t0 * c.K, rows,
                (int)c.K, (int)c.V, c.scale, ids, p, lp, f, ds->status);
     if (st != FP8RL_OK) return st;
@@ -576,7 +598,7 @@ fp8rl_status pack_rows(const Call& c, const Plan& pl, const DeviceState* ds, int
   va->tgt = r.tgt;
   va->K = (int)c.K;
   va->status = ds->status;
-  return launch(rows_kernel, (rows + r.rows_per_cta - 1) / r.rows_per_cta, kRowThreads, c.stream,
+  return launch(rows_kernel, dim3((unsigned)((rows + r.rows_per_cta - 1) / r.rows_per_cta)), kRowThreads, c.stream,
                 "rows_kernel launch", r);
 }
 
@@ -586,10 +608,10 @@ fp8rl_status launch_combine(const CombineArgs& b, int64_t rows, const DeviceStat
                             cudaStream_t stream) {
   const char* what = "combine_kernel launch";
   if (rows <= 2 * ds->sm_count)
-    return launch(combine_kernel<1>, rows, kCombineThreads, stream, what, b);
+    return launch(combine_kernel<1>, dim3((unsigned)rows), kCombineThreads, stream, what, b);
   if (rows <= 8 * ds->sm_count)
-    return launch(combine_kernel<4>, (rows + 3) / 4, kCombineThreads, stream, what, b);
-  return launch(combine_kernel<16>, (rows + 15) / 16, kCombineThreads, stream, what, b);
+    return launch(combine_kernel<4>, dim3((unsigned)((rows + 3) / 4)), kCombineThreads, stream, what, b);
+  return launch(combine_kernel<16>, dim3((unsigned)((rows + 15) / 16)), kCombineThreads, stream, what, b);
 }
 
 fp8rl_status run_forward(const Call& c) {
@@ -648,13 +670,18 @@ fp8rl_status run_backward(const Call& c, float coef) {
   va.dw = reinterpret_cast<__nv_bfloat16*>(c.grad_weight);
   if ((st = vocab_backward(va, ds, c.stream)) != FP8RL_OK) return st;
   if (c.grad_hidden) {
-    const bool shared = va.slices >= 8;
-    const int64_t per_cta = shared ? 32 : 256;
-    const int64_t ctas = (c.T * (c.H / 4) + per_cta - 1) / per_cta;
-    st = launch(shared ? scatter_kernel<8> : scatter_kernel<1>,
-                std::min<int64_t>(ctas, 16 * ds->sm_count), 256, c.stream, "scatter_kernel launch",
-                va.dx, va.n_rows, va.map, (int)c.H, va.slices, (int64_t)va.rows_pad * c.H,
-                va.lo_off, reinterpret_cast<__nv_bfloat16*>(c.grad_hidden));
+    __nv_bfloat16* gh = reinterpret_cast<__nv_bfloat16*>(c.grad_hidden);
+    if (va.slices >= 8 || va.lo_off) {
+      st = launch(scatter_few_kernel,
+                  dim3((unsigned)((c.H / 4 + 31) / 32), (unsigned)std::min<int64_t>(c.T, 4096)), 256,
+                  c.stream, "scatter_few_kernel launch", va.dx, va.n_rows, va.map, (int)c.H,
+                  va.slices, (int64_t)va.rows_pad * c.H, va.lo_off, gh);
+    } else {
+      const int64_t ctas = (c.T * (c.H / 8) + 255) / 256;
+      st = launch(scatter_kernel, dim3((unsigned)std::min<int64_t>(ctas, 8 * ds->sm_count)), 256,
+                  c.stream, "scatter_kernel launch", va.dx, va.n_rows, va.map, (int)c.H, va.slices,
+                  (int64_t)va.rows_pad * c.H, gh);
+    }
     if (st != FP8RL_OK) return st;
   }
   return ok();

@@ -48,8 +48,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const VocabArgs a) {
   extern __shared__ ulonglong2 xs[];      // [NT][2 planes][H / 8]: 4 floats each
   __shared__ int32_t sids[NT][kMaxK];
   __shared__ float wm[kWarps][NT], wr[kWarps][NT];
-  ptx::grid_dependents_launch();
   ptx::grid_dependency_wait();
+  ptx::grid_dependents_launch();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n = min(*a.n_rows, NT);
   const int vecs = a.H / 8, K = max(a.K, 1);

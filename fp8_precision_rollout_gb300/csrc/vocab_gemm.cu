@@ -32,6 +32,7 @@
 // vocabulary and G of the next, so that a launch has one tail, not three.
 // Every wait is bounded (1 s); see mbar_wait.
 #include <algorithm>
+#include <climits>
 #include <mutex>
 
 #include "sm100_ptx.cuh"
@@ -56,6 +57,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 // The tensor cores' FP32 sums of stats are cut into runs of this many steps,
 // added up in registers (see the stats epilogue).
 constexpr int kRun = 8;
+// Steps of W fetched into L2 while the rows are packed (about 35 MB in all).
+constexpr int kEarly = 16;
 
 enum Kind { kStats = 0, kGrad = 1, kDx = 2, kDw = 3 };
 
@@ -100,6 +103,7 @@ struct Params {
   int vc_prod;     // its columns
   int dx_tiles_n;  // column tiles of H when dX / dW are wanted, else 0
   int dw_tiles_n;
+  int early;       // fetch W before the packed rows are there
   int dx_first;    // this piece's dX is stored, not added
 };
 
@@ -201,15 +205,51 @@ __device__ __forceinline__ bool get_job(const Params& p, const Schedule& s, int 
   return true;
 }
 
-// First of this row's entries with id >= v.
-__device__ __forceinline__ int first_entry(const int32_t* ids, int K, int v) {
-  int lo = 0, hi = K;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(ids + mid) < v) lo = mid + 1; else hi = mid;
+// This row's entries from a vocabulary column on, in ascending order, four of
+// them loaded ahead: one dependent load after the other, the 20 entries of a
+// dense row took longer than a short tile's products.
+struct Entries {
+  int cur;          // index of id[0]
+  int32_t id[4];    // INT_MAX past the end
+  float p[4];
+  int64_t at;
+  __device__ __forceinline__ void none() {
+    cur = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      id[i] = INT_MAX;
+      p[i] = 0.0f;
+    }
+    at = 0;
   }
-  return lo;
-}
+  // first entry with id >= v
+  __device__ __forceinline__ void find(const VocabArgs& a, int row, int v) {
+    at = (int64_t)a.map[row] * a.K;
+    int lo = 0, hi = a.K;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(a.ids + at + mid) < v) lo = mid + 1; else hi = mid;
+    }
+    cur = lo;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) id[i] = cur + i < a.K ? __ldg(a.ids + at + cur + i) : INT_MAX;
+  }
+  __device__ __forceinline__ void find_p(const VocabArgs& a) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = cur + i < a.K ? __ldg(a.p + at + cur + i) : 0.0f;
+  }
+  __device__ __forceinline__ void next(const VocabArgs& a, bool with_p) {
+    ++cur;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      id[i] = id[i + 1];
+      p[i] = p[i + 1];
+    }
+    const bool more = cur + 3 < a.K;
+    id[3] = more ? __ldg(a.ids + at + cur + 3) : INT_MAX;
+    if (with_p) p[3] = more ? __ldg(a.p + at + cur + 3) : 0.0f;
+  }
+};
 
 template <bool kFwd>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
@@ -238,8 +278,21 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     st->abort_flag = 0;
     mbar_fence_init();
   }
-  grid_dependents_launch();
+  if (warp == 0 && elect_one()) {
+    tma_prefetch_map(&p.x_k);
+    tma_prefetch_map(&p.w_k);
+    // With one row tile the first job is known without the row count.  The
+    // kernel before this one (rows_kernel) lets it start only after what came
+    // earlier in the stream has completed, so W may be read already: the first
+    // job's first steps come into L2 while the rows are packed.
+    if (p.early) {
+      const int wrow = (kFwd ? 0 : p.v_grad) + (int)(blockIdx.x >> 1) * p.tn + (int)rank * (p.tn / 2);
+      if (wrow < a.V)
+        for (int k = 0; k < kEarly && k * kBK < a.H; ++k) tma_prefetch_l2_2d(&p.w_k, k * kBK, wrow);
+    }
+  }
   grid_dependency_wait();
+  grid_dependents_launch();
   // both CTAs' barriers exist before either CTA's work refers to them
   __syncthreads();
   cluster_arrive();
@@ -372,12 +425,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         // a bias that grows with the length of the run.
         const bool ok = row < n;
         const int32_t tgt = (ok && a.K == 0) ? a.tgt[row] - col0 : -1;   // in [0, hw) if here
-        const int32_t* ids = nullptr;
-        int cur = 0;
-        if (ok && a.K) {
-          ids = a.ids + (int64_t)a.map[row] * a.K;
-          cur = first_entry(ids, a.K, col0);
-        }
+        Entries en;
+        en.none();
+        if (ok && a.K) en.find(a, row, col0);
         float acc[128];
         for (int k = 0; k < j.steps; k += kRun, ++use) {
           const uint32_t buf = use & 1u;
@@ -436,15 +486,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             for (int e = 0; e < 128; ++e) z = tgt == e ? acc[e] : z;
             if (tgt >= 0 && tgt < hw) a.zt[row] = z;
           }
-          if (ids) {
-            for (; cur < a.K; ++cur) {
-              const int32_t rel = __ldg(ids + cur) - col0;
-              if (rel >= hw) break;
-              float z = 0.0f;
+          while (en.id[0] - col0 < hw) {
+            const int rel = en.id[0] - col0;
+            float z = 0.0f;
 #pragma unroll
-              for (int e = 0; e < 128; ++e) z = rel == e ? acc[e] : z;
-              a.zt[(int64_t)row * a.K + cur] = z;
-            }
+            for (int e = 0; e < 128; ++e) z = rel == e ? acc[e] : z;
+            a.zt[(int64_t)row * a.K + en.cur] = z;
+            en.next(a, false);
           }
           __syncwarp();
         }
@@ -454,9 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const bool ok = row < n;
         float gc = 0.0f, nl = 0.0f;
         int32_t tgt = -1;
-        const int32_t* ids = nullptr;
-        const float* pr = nullptr;
-        int cur = 0;
+        Entries en;
+        en.none();
         const int vcol = p.v_grad + col0;    // grad: vocabulary column
         if (j.kind == kGrad && ok) {
           gc = a.gcoef[row];
@@ -464,10 +511,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           if (a.K == 0) {
             tgt = a.tgt[row] - vcol;
           } else {
-            const int64_t at = (int64_t)a.map[row] * a.K;
-            ids = a.ids + at;
-            pr = a.p + at;
-            cur = first_entry(ids, a.K, vcol);
+            en.find(a, row, vcol);
+            en.find_p(a);
           }
         }
         bool okw = mbar_wait(smem_u32(&st->tfull[buf]), (use >> 1) & 1u, abort_flag, a.status, 55);
@@ -528,14 +573,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
                 for (int e = 0; e < 32; ++e) f[e] = rel == e ? f[e] - 1.0f : f[e];
               }
-              if (ids) {
-                for (; cur < a.K; ++cur) {
-                  const int32_t re = __ldg(ids + cur) - vcol - c * 32;
-                  if (re >= 32) break;
-                  const float pp = __ldg(pr + cur);
+              while (en.id[0] - vcol < min(hw, (c + 1) * 32)) {
+                const int re = en.id[0] - vcol - c * 32;
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) f[e] = re == e ? f[e] - pp : f[e];
-                }
+                for (int e = 0; e < 32; ++e) f[e] = re == e ? f[e] - en.p[0] : f[e];
+                en.next(a, true);
               }
               __syncwarp();
               const int live = ok ? a.V - (vcol + c * 32) : 0;   // columns that exist
@@ -679,7 +721,7 @@ int vocab_dx_slices(int64_t rows, int64_t H, int64_t vc) {
 namespace {
 
 // Columns of the head tiles (stats, grad) for `mt` row tiles x V columns on
-// `pairs` pairs of SMs: the width, a multiple of `unit` from 64 on, whose rounds
+// `pairs` pairs of SMs: the width, a multiple of 32 from 64 on, whose rounds
 // take the least time, a round counted as its width plus 16 columns' worth of
 // overhead.  With many rounds that is the full width (and nothing else is
 // looked at from kNarrowTiles tiles on); with few, a narrower tile keeps the
@@ -687,11 +729,11 @@ namespace {
 // rounds on 76 pairs, or two rounds of 224.
 constexpr int kNarrowTiles = 600, kNarrowest = 64;
 
-int head_tile(int64_t mt, int64_t V, int pairs, int unit) {
+int head_tile(int64_t mt, int64_t V, int pairs) {
   if (mt * tiles(V) > kNarrowTiles) return kTile;
   int best = kTile;
   int64_t cost = INT64_MAX;
-  for (int tn = kTile; tn >= kNarrowest; tn -= unit) {
+  for (int tn = kTile; tn >= kNarrowest; tn -= 32) {
     const int64_t rounds = (mt * ((V + tn - 1) / tn) + pairs - 1) / pairs;
     const int64_t c = rounds * (tn + 16);
     if (c < cost) {
@@ -708,7 +750,7 @@ int vocab_parts(const VocabArgs& a, const DeviceState* ds) {
   if (vocab_few(a.rows_cap, a.H)) return ds->sm_count;
   int pairs = 1;
   pairs_of<true>(ds, &pairs);
-  const int half = head_tile(a.rows_pad / kTile, a.V, pairs, 32) / 2;
+  const int half = head_tile(a.rows_pad / kTile, a.V, pairs) / 2;
   return (a.V + half - 1) / half;
 }
 
@@ -725,7 +767,8 @@ fp8rl_status vocab_forward(const VocabArgs& a, const DeviceState* ds, cudaStream
   int pairs = 0;
   fp8rl_status st = pairs_of<true>(ds, &pairs);
   if (st != FP8RL_OK) return st;
-  p.tn = head_tile(a.rows_pad / kTile, a.V, pairs, 32);
+  p.tn = head_tile(a.rows_pad / kTile, a.V, pairs);
+  p.early = a.rows_pad == kTile;
   if ((st = map_bf16(&p.x_k, a.x, a.H, a.rows_pad, a.H, 128, "hidden")) != FP8RL_OK) return st;
   if ((st = map_bf16(&p.w_k, a.w, a.H, a.V, a.ldw, p.tn / 2, "weight")) != FP8RL_OK) return st;
   return launch<true>(p, tiles(a.rows_cap) * ((a.V + p.tn - 1) / p.tn), ds, stream);
@@ -740,8 +783,7 @@ fp8rl_status vocab_backward(const VocabArgs& a, const DeviceState* ds, cudaStrea
   const int64_t mt = tiles(a.rows_pad), ht = tiles(a.H);
   int pairs = 0;
   if ((st = pairs_of<false>(ds, &pairs)) != FP8RL_OK) return st;
-  // (multiples of 64, so that G's columns are written to the end of dX's last step)
-  p.tn = pieces == 1 ? head_tile(mt, a.V, pairs, 64) : kTile;
+  p.tn = pieces == 1 ? head_tile(mt, a.V, pairs) : kTile;
   if ((st = map_bf16(&p.x_k, a.x, a.H, a.rows_pad, a.H, 128, "hidden")) != FP8RL_OK) return st;
   if ((st = map_bf16(&p.w_k, a.w, a.H, a.V, a.ldw, p.tn / 2, "weight")) != FP8RL_OK) return st;
   if ((st = map_bf16(&p.x_mn, a.x, a.H, a.rows_pad, a.H, 64, "hidden")) != FP8RL_OK) return st;
@@ -768,11 +810,14 @@ fp8rl_status vocab_backward(const VocabArgs& a, const DeviceState* ds, cudaStrea
   }
   for (int64_t i = 0; i <= pieces; ++i) {
     int64_t jobs = 0;
+    p.early = i == 0 && a.rows_pad == kTile;
     p.n_grad = p.dx_tiles_n = p.dw_tiles_n = 0;
     p.vc_prod = 0;
     if (i < pieces) {
       p.v_grad = (int)(i * a.vc);
-      p.n_grad = (int)((std::min<int64_t>(a.vc, a.V - p.v_grad) + p.tn - 1) / p.tn);
+      // (to a multiple of 64 columns, zeros past the vocabulary: dX sums whole steps)
+      const int64_t cols = (std::min<int64_t>(a.vc, a.V - p.v_grad) + kBK - 1) / kBK * kBK;
+      p.n_grad = (int)((cols + p.tn - 1) / p.tn);
       p.g_row = a.g[i & 1];
       p.g_out = g_out[i & 1];
       jobs += mt * p.n_grad;
