@@ -90,11 +90,12 @@ constexpr size_t smem_bytes() {
 static_assert(smem_bytes<true>() <= 232448 && smem_bytes<false>() <= 232448, "shared memory budget");
 
 struct Params {
-  CUtensorMap x_k, w_k;             // stats, grad: boxes 64 x 128 rows
+  CUtensorMap x_k[2], w_k;          // stats, grad: X's rows of the even and the odd CTA
   CUtensorMap g_out;                // grad: the piece written (32 x 64 boxes)
   CUtensorMap g_k, w_mn, dx_out;    // dX
   CUtensorMap g_mn, x_mn, dw_out;   // dW
   VocabArgs a;
+  int x_rows[2];   // rows of the boxes of x_k; 0: nothing to load
   int tn;          // stats, grad: columns of a tile, a multiple of 32 up to kTile
   int v_grad;      // first vocabulary column of the grad piece
   int n_grad;      // its column tiles (0: none)
@@ -156,6 +157,11 @@ __device__ __forceinline__ Schedule make_schedule(const Params& p, int n, int c,
 // kBand row tiles, rows fastest: a column tile of W is used by the whole band
 // at once and the band's rows of X stay in L2.
 __device__ __forceinline__ void band_tile(int t, int mt, int tiles_n, int* m, int* nn) {
+  if (mt == 1) {            // (no divisions on the way to a short call's first load)
+    *m = 0;
+    *nn = t;
+    return;
+  }
   const int per_band = kBand * tiles_n;
   const int band = t / per_band;
   const int gs = min(kBand, mt - band * kBand);
@@ -203,6 +209,33 @@ __device__ __forceinline__ bool get_job(const Params& p, const Schedule& s, int 
     *j = {kGrad, h_steps, m * kTile, nn * p.tn, 0, 0};
   }
   return true;
+}
+
+// 2^x, within 2 ulp; results below the normal range become 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two FP32 operations at once, each rounded to nearest: a * b + c, a * b.
+__device__ __forceinline__ void fma2(float& x, float& y, float a0, float a1, float b, float c) {
+  asm("{\n\t.reg .b64 ra, rb, rc;\n\t"
+      "mov.b64 ra, {%2, %3};\n\t"
+      "mov.b64 rb, {%4, %4};\n\t"
+      "mov.b64 rc, {%5, %5};\n\t"
+      "fma.rn.f32x2 rc, ra, rb, rc;\n\t"
+      "mov.b64 {%0, %1}, rc;\n\t}"
+      : "=f"(x), "=f"(y)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void mul2(float& x, float& y, float b) {
+  asm("{\n\t.reg .b64 ra, rb;\n\t"
+      "mov.b64 ra, {%0, %1};\n\t"
+      "mov.b64 rb, {%2, %2};\n\t"
+      "mul.rn.f32x2 ra, ra, rb;\n\t"
+      "mov.b64 {%0, %1}, ra;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(b));
 }
 
 // This row's entries from a vocabulary column on, in ascending order, four of
@@ -279,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     mbar_fence_init();
   }
   if (warp == 0 && elect_one()) {
-    tma_prefetch_map(&p.x_k);
+    tma_prefetch_map(&p.x_k[rank]);
     tma_prefetch_map(&p.w_k);
     // With one row tile the first job is known without the row count.  The
     // kernel before this one (rows_kernel) lets it start only after what came
@@ -315,8 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       Job j;
       for (int i = 0; alive && get_job<kFwd>(p, sch, n, i, &j); ++i) {
         const bool head = kFwd || j.kind == kGrad;
-        // (a narrower head tile loads fewer rows of W)
-        const uint32_t bytes = head ? 2 * kOperand + p.tn * kBK * 2 : 2 * kStageBytes;
+        // (a narrower head tile loads fewer rows of W, one with few rows fewer of X)
+        const uint32_t bytes = head ? (p.x_rows[0] + p.x_rows[1] + p.tn) * kBK * 2 : 2 * kStageBytes;
         const int wrow = (kFwd ? 0 : p.v_grad) + j.b0 + (int)rank * (p.tn / 2);
         for (int k = 0; k < j.steps; ++k, ++it) {
           const int s = it % STAGES;
@@ -330,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             const uint32_t da = s_base + s * kStageBytes, db = da + kOperand;
             const int kk = j.k0 + k * kBK;
             if (head) {
-              tma_load_2d_pair(da, &p.x_k, fb, kk, j.a0 + half);
+              if (p.x_rows[rank]) tma_load_2d_pair(da, &p.x_k[rank], fb, kk, j.a0 + half);
               tma_load_2d_pair(db, &p.w_k, fb, kk, wrow);
             } else if (j.kind == kDx) {
               tma_load_2d_pair(da, &p.g_k, fb, kk, j.a0 + half);
@@ -474,7 +507,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           float s0 = 0.0f, s1 = 0.0f, ties = 0.0f;
 #pragma unroll
           for (int e = 0; e < 128; e += 2) {
-            const float e0 = exp2f(fmaf(acc[e], k2, base)), e1 = exp2f(fmaf(acc[e + 1], k2, base));
+            float e0, e1;
+            fma2(e0, e1, acc[e], acc[e + 1], k2, base);
+            e0 = ex2(e0);
+            e1 = ex2(e1);
             if (acc[e] == mx) ties += 1.0f; else s0 += e0;
             if (acc[e + 1] == mx) ties += 1.0f; else s1 += e1;
           }
@@ -567,7 +603,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[e]);
             if (j.kind == kGrad) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) f[e] = exp2f(fmaf(f[e], k2, nl));
+              for (int e = 0; e < 32; e += 2) {
+                fma2(f[e], f[e + 1], f[e], f[e + 1], k2, nl);
+                f[e] = ex2(f[e]);
+                f[e + 1] = ex2(f[e + 1]);
+              }
               const int32_t rel = tgt - c * 32;
               if (__any_sync(0xFFFFFFFFu, rel >= 0 && rel < 32)) {
 #pragma unroll
@@ -580,10 +620,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 en.next(a, true);
               }
               __syncwarp();
-              const int live = ok ? a.V - (vcol + c * 32) : 0;   // columns that exist
 #pragma unroll
-              for (int e = 0; e < 32; ++e) f[e] = e < live ? gc * f[e] : 0.0f;
-              if (a.lo_off && row >= a.lo_off) {
+              for (int e = 0; e < 32; e += 2) mul2(f[e], f[e + 1], gc);
+              // rows past the last and columns past the vocabulary are zero
+              const int live = ok ? a.V - (vcol + c * 32) : 0;
+              if (__any_sync(0xFFFFFFFFu, live < 32)) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) f[e] = e < live ? f[e] : 0.0f;
+              }
+              if (a.lo_off && row0 + 31 >= a.lo_off) {    // (a multiple of 32: the warp's rows are all of one kind)
 #pragma unroll
                 for (int e = 0; e < 32; ++e) f[e] -= __bfloat162float(__float2bfloat16_rn(f[e]));
               }
@@ -649,6 +694,23 @@ fp8rl_status map_bf16(CUtensorMap* m, const void* base, int64_t inner, int64_t r
                       uint32_t box_rows, const char* what) {
   return encode_tiled_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, (uint64_t)inner, (uint64_t)rows,
                          (uint64_t)ld * 2, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B, what);
+}
+
+// X's boxes: the tile's 128 rows per CTA.  Where there is one row tile, only the
+// rows it has, to a multiple of 8: the copy engine takes about 2.3 cycles for
+// each 128-byte row, whether it holds anything or not, and with W's rows alone
+// it keeps up with HBM.  (What lies in shared memory instead belongs to rows
+// of the product that nobody reads.)
+fp8rl_status map_x(Params* p, const VocabArgs& a) {
+  const int rows = a.lo_off + a.rows_cap;
+  for (int r = 0; r < 2; ++r) {
+    p->x_rows[r] = 128;
+    if (a.rows_pad == kTile) p->x_rows[r] = std::min(128, std::max(0, (rows - 128 * r + 7) / 8 * 8));
+    const fp8rl_status st =
+        map_bf16(&p->x_k[r], a.x, a.H, a.rows_pad, a.H, (uint32_t)std::max(8, p->x_rows[r]), "hidden");
+    if (st != FP8RL_OK) return st;
+  }
+  return FP8RL_OK;
 }
 
 // Sets the shared-memory attribute once per device and asks how many CTA
@@ -769,7 +831,7 @@ fp8rl_status vocab_forward(const VocabArgs& a, const DeviceState* ds, cudaStream
   if (st != FP8RL_OK) return st;
   p.tn = head_tile(a.rows_pad / kTile, a.V, pairs);
   p.early = a.rows_pad == kTile;
-  if ((st = map_bf16(&p.x_k, a.x, a.H, a.rows_pad, a.H, 128, "hidden")) != FP8RL_OK) return st;
+  if ((st = map_x(&p, a)) != FP8RL_OK) return st;
   if ((st = map_bf16(&p.w_k, a.w, a.H, a.V, a.ldw, p.tn / 2, "weight")) != FP8RL_OK) return st;
   return launch<true>(p, tiles(a.rows_cap) * ((a.V + p.tn - 1) / p.tn), ds, stream);
 }
@@ -784,7 +846,7 @@ fp8rl_status vocab_backward(const VocabArgs& a, const DeviceState* ds, cudaStrea
   int pairs = 0;
   if ((st = pairs_of<false>(ds, &pairs)) != FP8RL_OK) return st;
   p.tn = pieces == 1 ? head_tile(mt, a.V, pairs) : kTile;
-  if ((st = map_bf16(&p.x_k, a.x, a.H, a.rows_pad, a.H, 128, "hidden")) != FP8RL_OK) return st;
+  if ((st = map_x(&p, a)) != FP8RL_OK) return st;
   if ((st = map_bf16(&p.w_k, a.w, a.H, a.V, a.ldw, p.tn / 2, "weight")) != FP8RL_OK) return st;
   if ((st = map_bf16(&p.x_mn, a.x, a.H, a.rows_pad, a.H, 64, "hidden")) != FP8RL_OK) return st;
   if ((st = map_bf16(&p.w_mn, a.w, a.H, a.V, a.ldw, 64, "weight")) != FP8RL_OK) return st;
@@ -801,12 +863,12 @@ fp8rl_status vocab_backward(const VocabArgs& a, const DeviceState* ds, cudaStrea
                               CU_TENSOR_MAP_SWIZZLE_128B, "dX")) != FP8RL_OK)
       return st;
   } else {
-    p.dx_out = p.x_k;
+    p.dx_out = p.x_mn;
   }
   if (a.dw) {
     if ((st = map_bf16(&p.dw_out, a.dw, a.H, a.V, a.H, 32, "grad_weight")) != FP8RL_OK) return st;
   } else {
-    p.dw_out = p.x_k;
+    p.dw_out = p.x_mn;
   }
   for (int64_t i = 0; i <= pieces; ++i) {
     int64_t jobs = 0;
