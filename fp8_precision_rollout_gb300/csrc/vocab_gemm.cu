@@ -91,7 +91,7 @@ static_assert(smem_bytes<true>() <= 232448 && smem_bytes<false>() <= 232448, "sh
 
 struct Params {
   CUtensorMap x_k[2], w_k;          // stats, grad: X's rows of the even and the odd CTA
-  CUtensorMap g_out;                // grad: the piece written (32 x 64 boxes)
+  CUtensorMap g_out;                // grad: the piece written (32 x 32 boxes)
   CUtensorMap g_k, w_mn, dx_out;    // dX
   CUtensorMap g_mn, x_mn, dw_out;   // dW
   VocabArgs a;
@@ -562,7 +562,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         // the previous job's stores have read the staging buffer
         if (lane == 0) bulk_wait_read_all();
         __syncwarp();
-#pragma unroll
+        // (not unrolled: the code of four chunks of three kinds would miss the
+        // instruction cache all through a short launch)
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t v[32];
           tmem_ld32(tm + buf * kTile + c * 32, v);
@@ -633,40 +635,49 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 for (int e = 0; e < 32; ++e) f[e] -= __bfloat162float(__float2bfloat16_rn(f[e]));
               }
             }
-            // BF16 boxes of 64 columns; a narrow G tile, whose halves are no whole
-            // boxes, is stored from the registers
-            const uint32_t box = stg + (c >> 1) * kBoxBytes;
-            const bool direct = j.kind == kGrad && hw != kTile / 2;
-            __nv_bfloat16* grow = p.g_row + (int64_t)row * a.vc + col0 + c * 32;
+            uint32_t o[16];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              __nv_bfloat162 b0 = __floats2bfloat162_rn(f[e * 8], f[e * 8 + 1]);
-              __nv_bfloat162 b1 = __floats2bfloat162_rn(f[e * 8 + 2], f[e * 8 + 3]);
-              __nv_bfloat162 b2 = __floats2bfloat162_rn(f[e * 8 + 4], f[e * 8 + 5]);
-              __nv_bfloat162 b3 = __floats2bfloat162_rn(f[e * 8 + 6], f[e * 8 + 7]);
-              const int chunk = (c & 1) * 4 + e;
-              if (direct) {
-                uint4 o = {*reinterpret_cast<uint32_t*>(&b0), *reinterpret_cast<uint32_t*>(&b1),
-                           *reinterpret_cast<uint32_t*>(&b2), *reinterpret_cast<uint32_t*>(&b3)};
-                if (c * 32 + e * 8 < hw && col0 + c * 32 + e * 8 < a.vc)
-                  *reinterpret_cast<uint4*>(grow + e * 8) = o;
-                continue;
-              }
-              st_shared_v4(box + (uint32_t)(lane * 128 + ((chunk ^ (lane & 7)) * 16)),
-                           *reinterpret_cast<uint32_t*>(&b0), *reinterpret_cast<uint32_t*>(&b1),
-                           *reinterpret_cast<uint32_t*>(&b2), *reinterpret_cast<uint32_t*>(&b3));
+            for (int e = 0; e < 16; ++e) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(f[e * 2], f[e * 2 + 1]);
+              o[e] = *reinterpret_cast<const uint32_t*>(&b);
             }
-            if (!direct && (c & 1)) {
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                const int col = col0 + (c >> 1) * 64;
-                if (j.kind == kGrad) {
-                  tma_store_2d(&p.g_out, box, col, row0);
-                } else if (col < a.H && p.v_prod + row0 < a.V) {
-                  tma_store_2d(&p.dw_out, box, col, p.v_prod + row0);
+            if (j.kind == kGrad) {
+              // BF16 boxes of 32 columns (64-byte swizzle); half a box at the
+              // end of a narrow tile is stored from the registers
+              const int col = col0 + c * 32;
+              if (hw - c * 32 >= 32) {
+                const uint32_t box = stg + c * (kBoxBytes / 2);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  st_shared_v4(box + (uint32_t)(lane * 64 + ((e ^ ((lane >> 1) & 3)) * 16)), o[e * 4],
+                               o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                  if (col < a.vc) tma_store_2d(&p.g_out, box, col, row0);
+                  bulk_commit();
                 }
-                bulk_commit();
+              } else if (col < a.vc) {
+                uint4* to = reinterpret_cast<uint4*>(p.g_row + (int64_t)row * a.vc + col);
+                to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+              }
+            } else {
+              // BF16 boxes of 64 columns (128-byte swizzle)
+              const uint32_t box = stg + (c >> 1) * kBoxBytes;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                st_shared_v4(box + (uint32_t)(lane * 128 + ((((c & 1) * 4 + e) ^ (lane & 7)) * 16)),
+                             o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
+              if (c & 1) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                  const int col = col0 + (c >> 1) * 64;
+                  if (col < a.H && p.v_prod + row0 < a.V)
+                    tma_store_2d(&p.dw_out, box, col, p.v_prod + row0);
+                  bulk_commit();
+                }
               }
             }
           }
@@ -853,7 +864,10 @@ fp8rl_status vocab_backward(const VocabArgs& a, const DeviceState* ds, cudaStrea
   CUtensorMap g_out[2], g_k[2], g_mn[2];
   for (int i = 0; i < 2; ++i) {
     const void* g = a.g[i] ? a.g[i] : a.g[0];
-    if ((st = map_bf16(&g_out[i], g, a.vc, a.rows_pad, a.vc, 32, "G")) != FP8RL_OK) return st;
+    if ((st = encode_tiled_2d(&g_out[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g, (uint64_t)a.vc,
+                              (uint64_t)a.rows_pad, (uint64_t)a.vc * 2, 32, 32,
+                              CU_TENSOR_MAP_SWIZZLE_64B, "G")) != FP8RL_OK)
+      return st;
     if ((st = map_bf16(&g_k[i], g, a.vc, a.rows_pad, a.vc, 128, "G")) != FP8RL_OK) return st;
     if ((st = map_bf16(&g_mn[i], g, a.vc, a.rows_pad, a.vc, 64, "G")) != FP8RL_OK) return st;
   }
