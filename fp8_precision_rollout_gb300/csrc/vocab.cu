@@ -35,6 +35,7 @@ namespace {
 constexpr int kMaxTopK = 256;
 constexpr int kRowThreads = 256;
 constexpr int kTeacherWarps = 4;
+constexpr int kFusedEntries = 4096;
 
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
@@ -47,29 +48,37 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// One warp per token.  An entry is present if its id is in [0, V) and its
-// scaled logit is not -inf; NaN stays in the softmax and makes the row NaN.
-// Writes the entries in ascending id order (absent ones last, id INT_MAX,
-// p 0), and flags[t] = 0, or -1 for a token without entries.
-__global__ void __launch_bounds__(kTeacherWarps * 32)
-    teacher_kernel(const int32_t* ids, const float* logits, int64_t T, int K, int V, float scale,
-                   int32_t* ids_s, float* p_s, float* lp_s, int32_t* flags, uint32_t* status) {
-  __shared__ int32_t sid[kTeacherWarps][kMaxTopK];
-  __shared__ float su[kTeacherWarps][kMaxTopK];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t t = (int64_t)blockIdx.x * kTeacherWarps + warp;
-  ptx::grid_dependency_wait();
-  ptx::grid_dependents_launch();
-  if (t >= T) return;
-  int32_t* id = sid[warp];
-  float* u = su[warp];
+struct TeacherArgs {
+  const int32_t* ids;      // [T, K] as given
+  const float* logits;
+  int64_t T;
+  int K, V;
+  float scale;
+  int32_t* ids_s;          // [T, K] sorted
+  float* p_s;
+  float* lp_s;             // or null
+  int32_t* flags;          // [T]: 0, or -1 for a token without entries
+  uint32_t* status;
+};
+
+// An entry is present if its id is in [0, V) and its scaled logit is not -inf.
+__device__ __forceinline__ bool present(int32_t id, float scaled, int V) {
+  return id >= 0 && id < V && scaled != -INFINITY;
+}
+
+// One warp, one token: the softmax of its present entries (NaN stays in it and
+// makes the row NaN), written in ascending id order, absent entries last with
+// id INT_MAX and p 0.  id and u: kMaxTopK words of shared memory.  Returns
+// whether any entry is present.
+__device__ bool teacher_row(const TeacherArgs& a, int64_t t, int lane, int32_t* id, float* u) {
+  const int K = a.K;
   float mx = -INFINITY;
   bool any = false, bad = false;
   for (int j = lane; j < K; j += 32) {
-    const int32_t i = ids[t * K + j];
-    const float x = logits[t * K + j] * scale;
-    bad |= i >= V;
-    const bool there = i >= 0 && i < V && x != -INFINITY;
+    const int32_t i = a.ids[t * K + j];
+    const float x = a.logits[t * K + j] * a.scale;
+    bad |= i >= a.V;
+    const bool there = present(i, x, a.V);
     id[j] = there ? i : INT_MAX;
     u[j] = x;
     if (there) mx = fmaxf(mx, x);
@@ -77,7 +86,7 @@ __global__ void __launch_bounds__(kTeacherWarps * 32)
   }
   mx = warp_max(mx);
   any = __any_sync(0xFFFFFFFFu, any);
-  if (bad) atomicOr(status, kStatusBadIndex);
+  if (bad) atomicOr(a.status, kStatusBadIndex);
   __syncwarp();
   float s = 0.0f;
   for (int j = lane; j < K; j += 32)
@@ -89,15 +98,28 @@ __global__ void __launch_bounds__(kTeacherWarps * 32)
     int r = 0;
     for (int i = 0; i < K; ++i) r += (id[i] < mine || (id[i] == mine && i < j)) ? 1 : 0;
     const bool there = mine != INT_MAX;
-    ids_s[t * K + r] = mine;
-    p_s[t * K + r] = there ? expf(u[j] - mx) / s : 0.0f;
-    if (lp_s) lp_s[t * K + r] = there ? (u[j] - mx) - ls : 0.0f;
+    a.ids_s[t * K + r] = mine;
+    a.p_s[t * K + r] = there ? expf(u[j] - mx) / s : 0.0f;
+    if (a.lp_s) a.lp_s[t * K + r] = there ? (u[j] - mx) - ls : 0.0f;
   }
-  if (lane == 0) flags[t] = any ? 0 : -1;
+  return any;
+}
+
+__global__ void __launch_bounds__(kTeacherWarps * 32) teacher_kernel(const TeacherArgs a) {
+  __shared__ int32_t sid[kTeacherWarps][kMaxTopK];
+  __shared__ float su[kTeacherWarps][kMaxTopK];
+  ptx::grid_dependency_wait();
+  ptx::grid_dependents_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)blockIdx.x * kTeacherWarps + warp;
+  if (t >= a.T) return;
+  const bool any = teacher_row(a, t, lane, sid[warp], su[warp]);
+  if (lane == 0) a.flags[t] = any ? 0 : -1;
 }
 
 struct RowsArgs {
   const int32_t* flags;        // [T] target of each token; negative: left out
+  TeacherArgs teacher;         // kTeacher: instead of flags
   int64_t T;
   int V, H, rows_per_cta;
   const __nv_bfloat16* hidden; // [T, H], row stride ldh
@@ -105,7 +127,7 @@ struct RowsArgs {
   __nv_bfloat16* x;            // [rows_pad, H]
   int32_t* map;
   int32_t* tgt;
-  int32_t* n_rows;
+  int32_t* n_rows;             // [0]: rows of the products; [1]: kept tokens
   // forward: outputs of left-out tokens (0)
   float* out0;
   float* out1;
@@ -120,108 +142,155 @@ struct RowsArgs {
   uint32_t* status;
 };
 
+// A row of the products that belongs to no token.
+__device__ __forceinline__ void empty_row(const RowsArgs& a, int64_t r) {
+  a.map[r] = 0;
+  a.tgt[r] = -1;
+  a.lse_c[r] = 0.0f;
+  a.gcoef_c[r] = 0.0f;
+}
+
 // CTA b packs tokens [b*R, (b+1)*R): it counts the kept tokens before its
 // range itself (targets are 4 bytes, a row is 2H), so CTAs do not depend on
-// one another and the order is the tokens' order.
+// one another and the order is the tokens' order.  The hidden states are
+// loaded before it is known where they go.  With kTeacher (few tokens and
+// entries) R is 1 and the CTA also does its token's teacher_row.
+// Backward, dW sums over rows in steps of 64 and over both copies of them:
+// every row from the kept tokens' to the end of the last step is zero.  There
+// are as many rows after the kept tokens' as tokens left out, and the d-th of
+// those clears the d-th row from the end; rows past T are dealt to the CTAs.
+template <bool kTeacher>
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsArgs a) {
-  __shared__ int wsum[kRowThreads / 32];
+  constexpr int kWarps = kRowThreads / 32, kAhead = 4;
+  __shared__ int wsum[kWarps];
   __shared__ int idx[kRowThreads];
-  __shared__ int sbase;
+  __shared__ int own;
+  __shared__ int32_t sid[kTeacher ? kMaxTopK : 1];
+  __shared__ float su[kTeacher ? kMaxTopK : 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   ptx::grid_dependency_wait();
   ptx::grid_dependents_launch();
   const int64_t r0 = (int64_t)blockIdx.x * a.rows_per_cta;
   const int64_t r1 = min(a.T, r0 + a.rows_per_cta);
+  const int vecs = a.H / 8;
+  const bool ahead = (r1 - r0) * vecs <= kAhead * kRowThreads;
+  uint4 q[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    const int i = tid + k * kRowThreads, r = i / vecs;
+    if (ahead && r0 + r < r1)
+      q[k] = __ldg(reinterpret_cast<const uint4*>(a.hidden + (r0 + r) * a.ldh) + (i - r * vecs));
+  }
   int before = 0;
-  for (int64_t i = tid; i < r0; i += kRowThreads) {
-    const int32_t f = a.flags[i];
-    before += (f >= 0 && f < a.V) ? 1 : 0;
+  if (kTeacher) {
+    const TeacherArgs& te = a.teacher;
+    if (warp == 0) {
+      const bool any = teacher_row(te, r0, lane, sid, su);
+      if (lane == 0) own = any ? 0 : -1;
+    } else {
+      for (int64_t i = warp - 1; i < r0; i += kWarps - 1) {
+        bool any = false;
+        for (int j = lane; j < te.K; j += 32)
+          any |= present(te.ids[i * te.K + j], te.logits[i * te.K + j] * te.scale, te.V);
+        any = __any_sync(0xFFFFFFFFu, any);
+        if (lane == 0 && any) ++before;
+      }
+    }
+  } else {
+    for (int64_t i = tid; i < r0; i += kRowThreads) {
+      const int32_t f = a.flags[i];
+      before += (f >= 0 && f < a.V) ? 1 : 0;
+    }
   }
   before = __reduce_add_sync(0xFFFFFFFFu, before);
   if (lane == 0) wsum[warp] = before;
   __syncthreads();
-  if (tid == 0) {
-    int b = 0;
-    for (int w = 0; w < kRowThreads / 32; ++w) b += wsum[w];
-    sbase = b;
-  }
+  int base = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) base += wsum[w];
   __syncthreads();
-  int base = sbase;
-  const int vecs = a.H / 8;
   for (int64_t c0 = r0; c0 < r1; c0 += kRowThreads) {
     const int64_t t = c0 + tid;
-    const int32_t f = t < r1 ? a.flags[t] : -1;
+    const int32_t f = t < r1 ? (kTeacher ? own : a.flags[t]) : -1;
     const bool keep = f >= 0 && f < a.V;
     if (f >= a.V) atomicOr(a.status, kStatusBadIndex);
     const unsigned bal = __ballot_sync(0xFFFFFFFFu, keep);
     if (lane == 0) wsum[warp] = __popc(bal);
     __syncthreads();
-    int c = base + __popc(bal & ((1u << lane) - 1u));
+    int c = base + __popc(bal & ((1u << lane) - 1u));   // kept tokens before t
     int total = 0;
-    for (int w = 0; w < kRowThreads / 32; ++w) {
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
       if (w < warp) c += wsum[w];
       total += wsum[w];
     }
-    idx[tid] = keep ? c : -1;
-    if (keep) {
-      a.map[c] = (int32_t)t;
-      a.tgt[c] = f;
-      if (a.grad) {
-        a.lse_c[c] = a.lse[t];
-        a.gcoef_c[c] = a.grad[t] * a.coef;
+    if (t < r1) {
+      // kept: row c.  Left out: the row from the end that it clears, as ~row
+      idx[tid] = keep ? c : ~(int)(a.T - 1 - (t - c));
+      if (keep) {
+        a.map[c] = (int32_t)t;
+        a.tgt[c] = f;
+        if (a.grad) {
+          const float l = a.lse[t], g = a.grad[t] * a.coef;
+          a.lse_c[c] = l;
+          a.gcoef_c[c] = g;
+          if (a.lo_off) {
+            const int c2 = c + a.lo_off;
+            a.map[c2] = (int32_t)t;
+            a.tgt[c2] = f;
+            a.lse_c[c2] = l;
+            a.gcoef_c[c2] = g;
+          }
+        }
+      } else if (a.out0) {
+        a.out0[t] = 0.0f;
+        a.out1[t] = 0.0f;
+      } else if (a.lo_off) {
+        empty_row(a, ~idx[tid]);
       }
-      if (a.lo_off) {
-        const int c2 = c + a.lo_off;
-        a.map[c2] = (int32_t)t;
-        a.tgt[c2] = f;
-        a.lse_c[c2] = a.lse[t];
-        a.gcoef_c[c2] = a.grad[t] * a.coef;
-      }
-    } else if (t < r1 && a.out0) {
-      a.out0[t] = 0.0f;
-      a.out1[t] = 0.0f;
     }
     base += total;
     __syncthreads();
     const int here = (int)min((int64_t)kRowThreads, r1 - c0);
-    for (int i = tid; i < here * vecs; i += kRowThreads) {
-      const int r = i / vecs, v = i - r * vecs;
-      const int dst = idx[r];
-      if (dst >= 0) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.hidden + (c0 + r) * a.ldh) + v);
-        reinterpret_cast<uint4*>(a.x + (int64_t)dst * a.H)[v] = x;
-        if (a.lo_off) reinterpret_cast<uint4*>(a.x + (int64_t)(dst + a.lo_off) * a.H)[v] = x;
-      } else if (a.grad_hidden)
-        reinterpret_cast<uint4*>(a.grad_hidden + (c0 + r) * a.H)[v] = make_uint4(0, 0, 0, 0);
+    const auto put = [&](int r, int v, uint4 x) {
+      const bool kept = idx[r] >= 0;
+      const int64_t dst = kept ? idx[r] : ~idx[r];
+      if (!kept) {
+        if (!a.grad) return;
+        x = make_uint4(0, 0, 0, 0);
+        if (a.grad_hidden) reinterpret_cast<uint4*>(a.grad_hidden + (c0 + r) * a.H)[v] = x;
+      }
+      reinterpret_cast<uint4*>(a.x + dst * a.H)[v] = x;
+      if (a.lo_off) reinterpret_cast<uint4*>(a.x + (dst + a.lo_off) * a.H)[v] = x;
+    };
+    if (ahead) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = tid + k * kRowThreads, r = i / vecs;
+        if (r < here) put(r, i - r * vecs, q[k]);
+      }
+    } else {
+      for (int i = tid; i < here * vecs; i += kRowThreads) {
+        const int r = i / vecs, v = i - r * vecs;
+        put(r, v, __ldg(reinterpret_cast<const uint4*>(a.hidden + (c0 + r) * a.ldh) + v));
+      }
     }
     __syncthreads();
   }
-  if (r1 == a.T) {
-    // n_rows[0]: rows of the products; n_rows[1]: kept tokens
-    const int last = base && a.lo_off ? a.lo_off + base : base;
-    if (tid == 0) {
-      a.n_rows[0] = last;
-      a.n_rows[1] = base;
+  if (a.grad) {
+    // rows past T: between the copies, and to the end of the last step
+    const int64_t rows = a.lo_off ? a.lo_off + a.T : a.T;
+    const int64_t gap = a.lo_off ? a.lo_off - a.T : 0, tail = (rows + 63) / 64 * 64 - rows;
+    for (int64_t s = blockIdx.x; s < gap + tail; s += gridDim.x) {
+      const int64_t r = s < gap ? a.T + s : rows + (s - gap);
+      if (s < gap && tid == 0) empty_row(a, r);
+      for (int v = tid; v < vecs; v += kRowThreads)
+        reinterpret_cast<uint4*>(a.x + r * a.H)[v] = make_uint4(0, 0, 0, 0);
     }
-    if (a.grad) {
-      // dW sums over rows in steps of 64: the rows between the two copies and
-      // those that fill the last step are zero
-      if (base && a.lo_off) {
-        for (int c = base + tid; c < a.lo_off; c += kRowThreads) {
-          a.map[c] = 0;
-          a.tgt[c] = -1;
-          a.lse_c[c] = 0.0f;
-          a.gcoef_c[c] = 0.0f;
-        }
-        uint4* to = reinterpret_cast<uint4*>(a.x + (int64_t)base * a.H);
-        for (int64_t v = tid; v < (int64_t)(a.lo_off - base) * vecs; v += kRowThreads)
-          to[v] = make_uint4(0, 0, 0, 0);
-      }
-      const int end = (max(last, 1) + 63) / 64 * 64;
-      uint4* to = reinterpret_cast<uint4*>(a.x + (int64_t)last * a.H);
-      for (int64_t v = tid; v < (int64_t)(end - last) * vecs; v += kRowThreads)
-        to[v] = make_uint4(0, 0, 0, 0);
-    }
+  }
+  if (r1 == a.T && tid == 0) {
+    a.n_rows[0] = base && a.lo_off ? a.lo_off + base : base;
+    a.n_rows[1] = base;
   }
 }
 
@@ -251,21 +320,28 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
   __shared__ float sm[32][R], sr[32][R];
   ptx::grid_dependency_wait();
   ptx::grid_dependents_launch();
-  const int n = *a.n_rows;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int c0 = blockIdx.x * R;
-  if (c0 >= n) return;
   constexpr int kLanes = kCombineThreads / R;
   const float k2 = a.scale * 1.4426950408889634f;
+  // What needs no other load first: the row count, the first partials, and for
+  // the warps that finish a row its token and target logit.  (Rows past the
+  // last hold anything; they are read, as part of the workspace, and not used.)
+  const int n = *a.n_rows;
+  const int row = c0 + warp;
+  const bool finish = warp < R && row < a.rows_pad;
+  const int32_t token = finish ? a.map[row] : 0;
+  const float zt0 = finish && a.K == 0 ? a.zt[row] : 0.0f;
   float m = -INFINITY, r = -1.0f;
   const int c = c0 + tid % R;
-  if (c < n) {
+  if (c < a.rows_pad) {
     for (int i = tid / R; i < a.parts; i += kLanes * kCombineBatch) {
       float2 q[kCombineBatch];
 #pragma unroll
       for (int b = 0; b < kCombineBatch; ++b)
         q[b] = i + b * kLanes < a.parts ? a.part[(int64_t)(i + b * kLanes) * a.rows_pad + c]
                                         : make_float2(-INFINITY, -1.0f);
+      if (c >= n) break;
       // pairwise: three dependent joins a batch
 #pragma unroll
       for (int o = kCombineBatch / 2; o; o >>= 1)
@@ -273,6 +349,16 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
         for (int b = 0; b < o; ++b) vocab_join(q[b].x, q[b].y, q[b + o].x, q[b + o].y, k2);
       vocab_join(m, r, q[0].x, q[0].y, k2);
     }
+  }
+  if (c0 >= n) return;
+  const int64_t t = token;
+  const bool live = finish && row < n;
+  // a lane's first entry, loaded before the sums are joined
+  float p0 = 0.0f, lp0 = 0.0f, z0 = 0.0f;
+  if (live && lane < a.K) {
+    p0 = a.p[t * a.K + lane];
+    lp0 = a.lp[t * a.K + lane];
+    z0 = a.zt[(int64_t)row * a.K + lane];
   }
 #pragma unroll
   for (int o = R; o < 32; o <<= 1) {
@@ -288,8 +374,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
     sr[warp][lane] = r;
   }
   __syncthreads();
-  if (warp >= R || c0 + warp >= n) return;
-  const int row = c0 + warp;
+  if (!live) return;
   m = sm[lane][warp];
   r = sr[lane][warp];
 #pragma unroll
@@ -304,12 +389,13 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
   // nearly certain word, whose log-probability is close to -rest, keeps its
   // relative accuracy, and a certain one has exactly 0.
   const float ls = log1pf(r);
-  const int64_t t = a.map[row];
   float out = 0.0f;
   if (a.K == 0) {
-    out = __fsub_rn(__fmul_rn(a.zt[row] - m, a.scale), ls);
+    out = __fsub_rn(__fmul_rn(zt0 - m, a.scale), ls);
   } else {
-    for (int k = lane; k < a.K; k += 32) {
+    // (absent entries and those of probability 0 add nothing, whatever their logit)
+    if (p0 != 0.0f) out = p0 * (lp0 - __fsub_rn(__fmul_rn(z0 - m, a.scale), ls));
+    for (int k = lane + 32; k < a.K; k += 32) {
       const float p = a.p[t * a.K + k];
       if (p != 0.0f)
         out += p * (a.lp[t * a.K + k] -
@@ -545,27 +631,39 @@ fp8rl_status check_call(const Call& c, bool backward) {
 fp8rl_status pack_rows(const Call& c, const Plan& pl, const DeviceState* ds, int64_t t0,
                        int64_t rows, bool backward, float coef, VocabArgs* va) {
   char* ws = c.ws;
-  const int32_t* flags = c.K ? nullptr : c.targets + t0;
-  if (c.K) {
-    int32_t* f = reinterpret_cast<int32_t*>(ws + pl.flags);
-    int32_t* ids = reinterpret_cast<int32_t*>(ws + pl.ids);
-    float* p = reinterpret_cast<float*>(ws + pl.p);
-    float* lp = backward ? nullptr : reinterpret_cast<float*>(ws + pl.lp);
-    const fp8rl_status st =
-        launch(teacher_kernel, dim3((unsigned)((rows + kTeacherWarps - 1) / kTeacherWarps)), kTeacherWarps * 32,
-               c.stream, "teacher_kernel launch", c.ids + t0 * c.K, c.logits + t0 * c.K, rows,
-               (int)c.K, (int)c.V, c.scale, ids, p, lp, f, ds->status);
-    if (st != FP8RL_OK) return st;
-    flags = f;
-    va->ids = ids;
-    va->p = p;
-  }
   RowsArgs r = {};
-  r.flags = flags;
+  r.flags = c.K ? nullptr : c.targets + t0;
+  bool fused = false;
+  if (c.K) {
+    TeacherArgs te = {};
+    te.ids = c.ids + t0 * c.K;
+    te.logits = c.logits + t0 * c.K;
+    te.T = rows;
+    te.K = (int)c.K;
+    te.V = (int)c.V;
+    te.scale = c.scale;
+    te.ids_s = reinterpret_cast<int32_t*>(ws + pl.ids);
+    te.p_s = reinterpret_cast<float*>(ws + pl.p);
+    te.lp_s = backward ? nullptr : reinterpret_cast<float*>(ws + pl.lp);
+    te.flags = reinterpret_cast<int32_t*>(ws + pl.flags);
+    te.status = ds->status;
+    va->ids = te.ids_s;
+    va->p = te.p_s;
+    // one launch less where the CTAs' looks at the earlier tokens' entries are few
+    fused = rows <= 256 && rows * c.K <= kFusedEntries;
+    r.teacher = te;
+    if (!fused) {
+      const fp8rl_status st =
+          launch(teacher_kernel, dim3((unsigned)((rows + kTeacherWarps - 1) / kTeacherWarps)),
+                 kTeacherWarps * 32, c.stream, "teacher_kernel launch", te);
+      if (st != FP8RL_OK) return st;
+      r.flags = te.flags;
+    }
+  }
   r.T = rows;
   r.V = (int)c.V;
   r.H = (int)c.H;
-  r.rows_per_cta = (int)((rows + 4 * ds->sm_count - 1) / (4 * ds->sm_count));
+  r.rows_per_cta = (int)((rows + 4 * ds->sm_count - 1) / (4 * ds->sm_count));   // 1 if fused
   r.hidden = reinterpret_cast<const __nv_bfloat16*>(c.hidden) + t0 * c.ldh;
   r.ldh = c.ldh;
   r.x = reinterpret_cast<__nv_bfloat16*>(ws + pl.x);
@@ -598,7 +696,8 @@ fp8rl_status pack_rows(const Call& c, const Plan& pl, const DeviceState* ds, int
   va->tgt = r.tgt;
   va->K = (int)c.K;
   va->status = ds->status;
-  return launch(rows_kernel, dim3((unsigned)((rows + r.rows_per_cta - 1) / r.rows_per_cta)), kRowThreads, c.stream,
+  return launch(fused ? rows_kernel<true> : rows_kernel<false>,
+                dim3((unsigned)((rows + r.rows_per_cta - 1) / r.rows_per_cta)), kRowThreads, c.stream,
                 "rows_kernel launch", r);
 }
 

@@ -785,10 +785,10 @@ inline int64_t tiles(int64_t x) { return (x + kTile - 1) / kTile; }
 }  // namespace
 
 int vocab_dx_slices(int64_t rows, int64_t H, int64_t vc) {
-  // at least about two dX jobs per pair of SMs, each at least 8 steps deep
+  // as many as give each of 76 pairs of SMs at most one dX job, each at least 8
+  // steps deep (the pairs' other jobs even out the rest)
   const int64_t base = tiles(rows) * tiles(H);
-  const int64_t want = (152 + base - 1) / base;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(want, vc / (8 * kBK)));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(76 / base, vc / (8 * kBK)));
 }
 
 namespace {
