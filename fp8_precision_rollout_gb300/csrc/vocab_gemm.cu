@@ -51,12 +51,20 @@ constexpr int kOperand = 128 * kBK * 2;          // one operand's share of a CTA
 constexpr int kStageBytes = 2 * kOperand;
 constexpr int kBoxBytes = 4096;                  // output boxes: 32 rows x 128 bytes
 constexpr int kStageOutBytes = 2 * kBoxBytes;    // per epilogue warp
+constexpr int kPickLd = 33, kPickBytes = 32 * kPickLd * 4;   // the same; rows of 33 words: no bank conflicts
 constexpr int kMaxStages = 6;
 constexpr int kBand = 16;                        // row tiles per raster band
 constexpr float kLog2e = 1.4426950408889634f;
-// The tensor cores' FP32 sums of stats are cut into runs of this many steps,
-// added up in registers (see the stats epilogue).
-constexpr int kRun = 8;
+// The tensor cores' FP32 sums of stats are cut into runs of kRun steps, added up
+// in registers (see the stats epilogue); the first two runs of a tile are
+// longer, so that the tensor cores have work while the epilogue finishes the
+// tile before.
+constexpr int kRun = 8, kFirstRun = 12;
+__host__ __device__ constexpr int run_from(int k) { return k < 2 * kFirstRun ? kFirstRun : kRun; }
+__host__ __device__ constexpr bool run_starts(int k) {
+  return k < 2 * kFirstRun ? k % kFirstRun == 0 : (k - 2 * kFirstRun) % kRun == 0;
+}
+constexpr int kAheadFwd = 1, kAheadBwd = 4;   // entries loaded ahead (see Entries)
 // Steps of W fetched into L2 while the rows are packed (about 35 MB in all).
 constexpr int kEarly = 16;
 
@@ -71,7 +79,8 @@ constexpr uint32_t kMnA = 1u << 15, kMnB = 1u << 16;
 template <bool kFwd>
 struct Cfg {
   static constexpr int kStages = kFwd ? 6 : 5;
-  static constexpr size_t kOut = kFwd ? 0 : (size_t)kEpiWarps * kStageOutBytes;
+  // backward: output staging; stats: 32 columns of FP32 per epilogue thread
+  static constexpr size_t kOut = (size_t)kEpiWarps * (kFwd ? kPickBytes : kStageOutBytes);
 };
 
 struct Tail {
@@ -82,10 +91,10 @@ struct Tail {
   uint32_t tmem_base;
   uint32_t abort_flag;
 };
-static_assert(sizeof(Tail) <= 1024, "");
+constexpr size_t kTailBytes = (sizeof(Tail) + 15) / 16 * 16;
 template <bool kFwd>
 constexpr size_t smem_bytes() {
-  return 1024 + (size_t)Cfg<kFwd>::kStages * kStageBytes + Cfg<kFwd>::kOut + 1024;
+  return 1024 + (size_t)Cfg<kFwd>::kStages * kStageBytes + Cfg<kFwd>::kOut + kTailBytes;
 }
 static_assert(smem_bytes<true>() <= 232448 && smem_bytes<false>() <= 232448, "shared memory budget");
 
@@ -238,18 +247,19 @@ __device__ __forceinline__ void mul2(float& x, float& y, float b) {
       : "f"(b));
 }
 
-// This row's entries from a vocabulary column on, in ascending order, four of
+// This row's entries from a vocabulary column on, in ascending order, kD of
 // them loaded ahead: one dependent load after the other, the 20 entries of a
 // dense row took longer than a short tile's products.
+template <int kD>
 struct Entries {
-  int cur;          // index of id[0]
-  int32_t id[4];    // INT_MAX past the end
-  float p[4];
+  int cur;           // index of id[0]
+  int32_t id[kD];    // INT_MAX past the end
+  float p[kD];
   int64_t at;
   __device__ __forceinline__ void none() {
     cur = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kD; ++i) {
       id[i] = INT_MAX;
       p[i] = 0.0f;
     }
@@ -258,29 +268,35 @@ struct Entries {
   // first entry with id >= v
   __device__ __forceinline__ void find(const VocabArgs& a, int row, int v) {
     at = (int64_t)a.map[row] * a.K;
-    int lo = 0, hi = a.K;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(a.ids + at + mid) < v) lo = mid + 1; else hi = mid;
+    // eight probes at a time: two rounds of loads for 64 entries, not six
+    int lo = 0, len = a.K;
+    while (len > 0) {
+      const int step = (len + 7) >> 3;
+      int below = 0;
+#pragma unroll
+      for (int i = 1; i <= 8; ++i)
+        if (i * step <= len) below += __ldg(a.ids + at + lo + i * step - 1) < v ? 1 : 0;
+      lo += below * step;
+      len = min(step - 1, len - below * step);
     }
     cur = lo;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) id[i] = cur + i < a.K ? __ldg(a.ids + at + cur + i) : INT_MAX;
+    for (int i = 0; i < kD; ++i) id[i] = cur + i < a.K ? __ldg(a.ids + at + cur + i) : INT_MAX;
   }
   __device__ __forceinline__ void find_p(const VocabArgs& a) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = cur + i < a.K ? __ldg(a.p + at + cur + i) : 0.0f;
+    for (int i = 0; i < kD; ++i) p[i] = cur + i < a.K ? __ldg(a.p + at + cur + i) : 0.0f;
   }
   __device__ __forceinline__ void next(const VocabArgs& a, bool with_p) {
     ++cur;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < kD - 1; ++i) {
       id[i] = id[i + 1];
       p[i] = p[i + 1];
     }
-    const bool more = cur + 3 < a.K;
-    id[3] = more ? __ldg(a.ids + at + cur + 3) : INT_MAX;
-    if (with_p) p[3] = more ? __ldg(a.p + at + cur + 3) : 0.0f;
+    const bool more = cur + kD - 1 < a.K;
+    id[kD - 1] = more ? __ldg(a.ids + at + cur + kD - 1) : INT_MAX;
+    if (with_p) p[kD - 1] = more ? __ldg(a.p + at + cur + kD - 1) : 0.0f;
   }
 };
 
@@ -408,8 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const uint64_t db0 = b_mn ? sw128_desc_mn(s_base + kOperand, kOperand / 2) : sw128_desc(s_base + kOperand);
         const uint32_t qa = (a_mn ? 2048u : 32u) >> 4, qb = (b_mn ? 2048u : 32u) >> 4;
         for (int k = 0; k < j.steps; ++k, ++it) {
-          const bool fresh = k == 0 || (kFwd && k % kRun == 0);
-          const bool last = k + 1 == j.steps || (kFwd && (k + 1) % kRun == 0);
+          const bool fresh = k == 0 || (kFwd && run_starts(k));
+          const bool last = k + 1 == j.steps || (kFwd && run_starts(k + 1));
           const uint32_t buf = use & 1u;
           const int s = it % STAGES;
           if ((fresh && !mbar_wait(smem_u32(&st->tempty[buf]), ((use >> 1) & 1u) ^ 1u, abort_flag,
@@ -453,16 +469,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const int col0 = j.b0 + h * hw;
       const uint32_t tm = tmq + (uint32_t)(h * hw);
       if constexpr (kFwd) {
-        // Runs of kRun steps are summed on the tensor cores and the runs added
+        // Runs of steps are summed on the tensor cores and the runs added
         // here, rounded to nearest: the tensor cores truncate every addition,
         // a bias that grows with the length of the run.
         const bool ok = row < n;
         const int32_t tgt = (ok && a.K == 0) ? a.tgt[row] - col0 : -1;   // in [0, hw) if here
-        Entries en;
+        Entries<kAheadFwd> en;
         en.none();
         if (ok && a.K) en.find(a, row, col0);
         float acc[128];
-        for (int k = 0; k < j.steps; k += kRun, ++use) {
+        for (int k = 0; k < j.steps; k += run_from(k), ++use) {
           const uint32_t buf = use & 1u;
           bool okw = mbar_wait(smem_u32(&st->tfull[buf]), (use >> 1) & 1u, abort_flag, a.status, 54);
           okw = __all_sync(0xFFFFFFFFu, okw);
@@ -522,13 +538,24 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             for (int e = 0; e < 128; ++e) z = tgt == e ? acc[e] : z;
             if (tgt >= 0 && tgt < hw) a.zt[row] = z;
           }
-          while (en.id[0] - col0 < hw) {
-            const int rel = en.id[0] - col0;
-            float z = 0.0f;
+          // The entries' logits, 32 columns at a time through shared memory,
+          // where a thread can pick any of its own by index.
+          if (a.K) {
+            float* pick = reinterpret_cast<float*>(smem + STAGES * kStageBytes + (warp - 2) * kPickBytes) +
+                          lane * kPickLd;
 #pragma unroll
-            for (int e = 0; e < 128; ++e) z = rel == e ? acc[e] : z;
-            a.zt[(int64_t)row * a.K + en.cur] = z;
-            en.next(a, false);
+            for (int c = 0; c < 4; ++c) {
+              const int first = col0 + c * 32, end = col0 + min(hw, (c + 1) * 32);
+              if (__any_sync(0xFFFFFFFFu, en.id[0] < end)) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) pick[e] = acc[c * 32 + e];
+                while (en.id[0] < end) {
+                  a.zt[(int64_t)row * a.K + en.cur] = pick[en.id[0] - first];
+                  en.next(a, false);
+                }
+                __syncwarp();
+              }
+            }
           }
           __syncwarp();
         }
@@ -538,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const bool ok = row < n;
         float gc = 0.0f, nl = 0.0f;
         int32_t tgt = -1;
-        Entries en;
+        Entries<kAheadBwd> en;
         en.none();
         const int vcol = p.v_grad + col0;    // grad: vocabulary column
         if (j.kind == kGrad && ok) {
