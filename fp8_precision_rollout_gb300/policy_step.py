@@ -1,0 +1,105 @@
+"""One policy update of the output head, from hidden states to new rollout weights.
+
+    python -m fp8_precision_rollout_gb300.policy_step [--steps N] [--tokens T]
+
+The RL step that the FP8-RL summary describes around its importance weights
+(section 3.4.3), on synthetic hidden states: the rollout's log-probabilities
+come from a head whose weights went through the blockwise E4M3 quantizer, the
+trainer's from the BF16 head; their ratio gives the truncated importance
+weights and the mismatch statistics; the weighted policy-gradient loss and a
+distillation term towards a teacher's top entries are differentiated back to
+the hidden states and the head; the head is updated and quantized for the
+next rollout.  Every operation is a call of this library, except the
+teacher's top-k, the sampling and the optimizer's update, which are torch's.
+"""
+from __future__ import annotations
+
+import argparse
+
+import torch
+
+from . import binding as fp8rl
+
+
+class Head:
+    """BF16 head weights [vocab, hidden] with an FP32 master copy."""
+
+    def __init__(self, vocab: int, hidden: int, seed: int = 0, device="cuda"):
+        g = torch.Generator(device=device).manual_seed(seed)
+        self.master = torch.randn(vocab, hidden, generator=g, device=device) * hidden ** -0.5
+        self.weight = self.master.to(torch.bfloat16)
+
+    def rollout_weight(self) -> torch.Tensor:
+        """What the rollout engine multiplies with: the head after the per-step
+        E4M3 quantization (128 x 128 blocks), as BF16 values."""
+        q, scales = fp8rl.quantize_weights_blockwise(self.weight)
+        v, h = self.weight.shape
+        block = scales.repeat_interleave(128, 0)[:v].repeat_interleave(128, 1)[:, :h]
+        return (q.view(torch.float8_e4m3fn).float() * block).to(torch.bfloat16)
+
+    def update(self, grad_weight: torch.Tensor, lr: float):
+        self.master.add_(grad_weight.float(), alpha=-lr)
+        self.weight = self.master.to(torch.bfloat16)
+
+
+def policy_step(head: Head, hidden, targets, advantages, teacher_ids, teacher_logits,
+                distill_weight: float = 0.5, c_hi: float = 2.0):
+    """Loss terms and gradients of one batch: targets int32 [T] (negative:
+    prompt tokens, left out), advantages float32 [T].  Returns a dict with the
+    policy loss, the mean distillation loss, the mismatch statistics, and
+    grad_hidden / grad_weight of policy loss + distill_weight * distillation."""
+    logp_rollout, _ = fp8rl.token_logprobs(hidden, head.rollout_weight(), targets)
+    logp, lse = fp8rl.token_logprobs(hidden, head.weight, targets)
+    mask = (targets >= 0).to(torch.uint8)
+    # policy gradient with the importance weight held fixed: -w * A * logp
+    weights, stats = fp8rl.is_weights_stats(logp, logp_rollout, mask, c_hi, loss=-advantages * logp)
+    n = mask.sum().clamp(min=1)
+    gh, gw = fp8rl.token_logprobs_backward(hidden, head.weight, targets, lse,
+                                           -advantages * weights / n)
+    ids = torch.where(mask[:, None] != 0, teacher_ids, -1)
+    kl, kl_lse = fp8rl.distill_topk(hidden, head.weight, ids, teacher_logits)
+    scale = (distill_weight / n).expand(targets.numel()).float().contiguous()
+    dh, dw = fp8rl.distill_topk_backward(hidden, head.weight, ids, teacher_logits, kl_lse, scale)
+    return {"policy_loss": stats[5] / stats[0], "distill_loss": kl.sum() / n, "stats": stats,
+            "grad_hidden": gh.float() + dh.float(), "grad_weight": gw.float() + dw.float()}
+
+
+def synthetic_batch(tokens: int, vocab: int, hidden: int, top_k: int = 16, seed: int = 1,
+                    device="cuda"):
+    """Hidden states, sampled targets (the first quarter is a prompt), advantages
+    and a teacher's top entries (another random head's)."""
+    g = torch.Generator(device=device).manual_seed(seed)
+    x = torch.randn(tokens, hidden, generator=g, device=device).to(torch.bfloat16)
+    teacher = Head(vocab, hidden, seed=seed + 1, device=device)
+    logits, ids = (3.0 * x.float() @ teacher.master.T).topk(top_k, dim=1)
+    pick = torch.randint(0, top_k, (tokens, 1), generator=g, device=device)
+    targets = ids.gather(1, pick)[:, 0].to(torch.int32)
+    targets[: tokens // 4] = -1
+    advantages = torch.randn(tokens, generator=g, device=device)
+    return x, targets, advantages, ids.to(torch.int32), logits.contiguous()
+
+
+def main(argv=None):
+    ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
+    ap.add_argument("--steps", type=int, default=5)
+    ap.add_argument("--tokens", type=int, default=512)
+    ap.add_argument("--hidden", type=int, default=1024)
+    ap.add_argument("--vocab", type=int, default=32768)
+    ap.add_argument("--lr", type=float, default=0.5)
+    args = ap.parse_args(argv)
+    head = Head(args.vocab, args.hidden)
+    batch = synthetic_batch(args.tokens, args.vocab, args.hidden)
+    out = []
+    for step in range(args.steps):
+        r = policy_step(head, *batch)
+        out.append((float(r["policy_loss"]), float(r["distill_loss"])))
+        k1 = float(r["stats"][1] / r["stats"][0])
+        print("step %d  policy loss %+.5f  distillation %.5f  rollout mismatch (k1) %+.5f"
+              % (step, out[-1][0], out[-1][1], k1))
+        head.update(r["grad_weight"], args.lr)
+    fp8rl.device_status(0)
+    return out
+
+
+if __name__ == "__main__":
+    main()

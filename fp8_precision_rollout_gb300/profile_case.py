@@ -21,6 +21,10 @@ Cases (device footprint in parentheses):
                   one CTA per sequence and KV head, as at 64 x 20480)
   glue_gather     MoE gather + quantize: 4096 tokens x 2048 -> 32768 routed rows (0.1 GB)
   glue_silu       MoE SiLU(gate)*up + quantize: 32768 x 1536 -> 32768 x 768 (0.13 GB)
+  logprobs        token log-probabilities, 2048 tokens x 4096 x 32768 words (0.3 GB)
+  logprobs_one    the same of one token over 65536 words (0.5 GB)
+  logprobs_grad   their gradient, 1024 tokens x 4096 x 32768 words (0.7 GB)
+  distill         distillation from 64 teacher entries, 2048 tokens x 4096 x 32768 words (0.3 GB)
 """
 from __future__ import annotations
 
@@ -110,6 +114,22 @@ def main(argv=None):
     elif c == "glue_silu":
         h = wl.expert_inputs(wl.MOE_TOKENS * wl.MOE_TOPK, 2 * wl.MOE_INTER, seed=9, device=dev)
         run = lambda: fp8rl.silu_mul_quantize(h)  # noqa: E731
+    elif c in ("logprobs", "logprobs_one", "logprobs_grad", "distill"):
+        t, v = {"logprobs": (2048, 32768), "logprobs_one": (1, 65536), "logprobs_grad": (1024, 32768),
+                "distill": (2048, 32768)}[c]
+        h = wl.dense_acts(t, 4096, seed=10, device=dev)
+        w = wl.make_weight(v, 4096, seed=11, device=dev)
+        y = torch.randint(0, v, (t,), generator=torch.Generator().manual_seed(12)).to(torch.int32).to(dev)
+        if c == "distill":
+            ids = (y[:, None].long() + 97 * torch.arange(64, device=dev)) % v
+            u = -torch.cumsum(torch.rand(t, 64, device=dev), 1)
+            run = lambda: fp8rl.distill_topk(h, w, ids.to(torch.int32), u)  # noqa: E731
+        elif c == "logprobs_grad":
+            _, lse = fp8rl.token_logprobs(h, w, y)
+            up = torch.randn(t, device=dev)
+            run = lambda: fp8rl.token_logprobs_backward(h, w, y, lse, up)  # noqa: E731
+        else:
+            run = lambda: fp8rl.token_logprobs(h, w, y)  # noqa: E731
     else:
         raise SystemExit("unknown case %r" % c)
     for _ in range(args.iters):
