@@ -514,7 +514,8 @@ def vocab_workspace_bytes(tokens: int, hidden_dim: int, vocab: int, top_k: int =
 # what is wrong with it.
 
 def _head(hidden, weight):
-    if not (hidden.is_cuda and weight.is_cuda and hidden.dtype is torch.bfloat16
+    if not (isinstance(hidden, torch.Tensor) and isinstance(weight, torch.Tensor)
+            and hidden.is_cuda and weight.is_cuda and hidden.dtype is torch.bfloat16
             and weight.dtype is torch.bfloat16 and hidden.dim() == 2 and weight.dim() == 2
             and hidden.stride(1) == 1 and weight.stride(1) == 1):
         _rowmajor(_dev(hidden, torch.bfloat16, "hidden"), "hidden")
@@ -592,7 +593,7 @@ def token_logprobs(hidden, weight, targets, logit_scale: float = 1.0,
     s, current = _head_stream(stream, hidden)
     ws, size = _head_workspace(workspace, t, h, v, 0, 0, hidden, s, current)
     _check(load().fp8rl_token_logprobs(hidden.data_ptr(), ldh, weight.data_ptr(), ldw, tp, t, h, v,
-                                       logit_scale, logp.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+                                       float(logit_scale), logp.data_ptr(), lse.data_ptr(), ws.data_ptr(),
                                        size, s))
     return logp, lse
 
@@ -622,7 +623,7 @@ def token_logprobs_backward(hidden, weight, targets, lse, grad_logp, logit_scale
     s, current = _head_stream(stream, hidden)
     ws, size = _head_workspace(workspace, t, h, v, 0, 1, hidden, s, current)
     _check(load().fp8rl_token_logprobs_backward(
-        hidden.data_ptr(), ldh, weight.data_ptr(), ldw, tp, lp, gp, t, h, v, logit_scale,
+        hidden.data_ptr(), ldh, weight.data_ptr(), ldw, tp, lp, gp, t, h, v, float(logit_scale),
         None if gh is None else gh.data_ptr(), None if gw is None else gw.data_ptr(),
         ws.data_ptr(), size, s))
     return gh, gw
@@ -642,7 +643,7 @@ def distill_topk(hidden, weight, teacher_ids, teacher_logits, logit_scale: float
     s, current = _head_stream(stream, hidden)
     ws, size = _head_workspace(workspace, t, h, v, k, 0, hidden, s, current)
     _check(load().fp8rl_distill_topk(hidden.data_ptr(), ldh, weight.data_ptr(), ldw, ip, up, k, t,
-                                     h, v, logit_scale, loss.data_ptr(), lse.data_ptr(),
+                                     h, v, float(logit_scale), loss.data_ptr(), lse.data_ptr(),
                                      ws.data_ptr(), size, s))
     return loss, lse
 
@@ -664,7 +665,7 @@ def distill_topk_backward(hidden, weight, teacher_ids, teacher_logits, lse, grad
     s, current = _head_stream(stream, hidden)
     ws, size = _head_workspace(workspace, t, h, v, k, 1, hidden, s, current)
     _check(load().fp8rl_distill_topk_backward(
-        hidden.data_ptr(), ldh, weight.data_ptr(), ldw, ip, up, k, lp, gp, t, h, v, logit_scale,
+        hidden.data_ptr(), ldh, weight.data_ptr(), ldw, ip, up, k, lp, gp, t, h, v, float(logit_scale),
         None if gh is None else gh.data_ptr(), None if gw is None else gw.data_ptr(),
         ws.data_ptr(), size, s))
     return gh, gw

@@ -476,7 +476,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int32_t tgt = (ok && a.K == 0) ? a.tgt[row] - col0 : -1;   // in [0, hw) if here
         Entries<kAheadFwd> en;
         en.none();
-        if (ok && a.K) en.find(a, row, col0);
         float acc[128];
         for (int k = 0; k < j.steps; k += run_from(k), ++use) {
           const uint32_t buf = use & 1u;
@@ -505,6 +504,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
               for (int e = 0; e < 32; ++e) acc[c * 32 + e] += __uint_as_float(v[e]);
             }
           }
+          // (while the next run is on its way)
+          if (k == 0 && ok && a.K) en.find(a, row, col0);
+          __syncwarp();
         }
         if (!alive) break;
         if (col0 < a.V) {

@@ -214,6 +214,39 @@ def test_distillation_matches_the_oracle(t, h, v, k, mask):
     _check_grads(x, w, dense, kept, up, 1.0, scale, gh.view.view(t, h), gw.view.view(v, h))
 
 
+@pytest.mark.parametrize("t,h,v,k", [(8, 4096, 3001, 0), (5, 72, 1001, 9), (8, 256, 129, 256),
+                                     (70, 264, 33000, 0), (128, 64, 32768, 12), (130, 128, 16500, 3),
+                                     (389, 136, 20011, 0), (600, 64, 50021, 0), (600, 72, 40000, 70),
+                                     (1100, 128, 9000, 0), (4500, 64, 3000, 0)])
+def test_every_tile_width_and_row_count(t, h, v, k):
+    """Shapes by which path they take: a few tokens, one to eighteen row tiles, head
+    tiles of other widths than 256 (few rounds), entries in one launch and two."""
+    dev = device()
+    x, w, y, g = _head(t, h, v, dev, seed=11)
+    y[1::7] = -1
+    up = torch.randn(t, generator=g)
+    xd, wd, yd = x.to(dev), w.to(dev), y.to(dev)
+    if k == 0:
+        logp, lse = fp8rl.token_logprobs(xd, wd, yd)
+        gh, gw = fp8rl.token_logprobs_backward(xd, wd, yd, lse, up.to(dev))
+        _check_logp(x, w, y, logp, lse, 1.0)
+        d, kept = oracle.one_hot_targets(y.numpy(), v)
+        sign = -1.0
+    else:
+        ids, u = _teacher(t, k, v, y, g)
+        loss, lse = fp8rl.distill_topk(xd, wd, ids.to(dev), u.to(dev))
+        gh, gw = fp8rl.distill_topk_backward(xd, wd, ids.to(dev), u.to(dev), lse, up.to(dev))
+        ref, rl = oracle.distill_topk(x, w, ids.numpy(), u.numpy())
+        dz, ev = _bounds(x, w, 1.0)
+        p, lp, there, kept = oracle.teacher_entries(ids.numpy(), u.numpy(), v)
+        _close32(lse, rl, dz + ev, "lse")
+        assert (np.abs(_np(loss) - ref) <= 2 * dz + 3 * (ev + 256 * 2.0 ** -24 * np.abs(lp).max(axis=1))).all()
+        d, sign = oracle.dense_teacher(ids.numpy(), p, there, v), 1.0
+    torch.cuda.synchronize()
+    fp8rl.device_status(0)
+    _check_grads(x, w, d, kept, up, sign, 1.0, gh, gw)
+
+
 def test_pieces_of_tokens_and_of_the_vocabulary():
     """More tokens than one forward piece holds, and a G that takes several
     vocabulary pieces; sampled rows and columns against the oracle."""
@@ -359,6 +392,8 @@ def test_row_strides_and_single_outputs():
         fp8rl.token_logprobs(x.to(dev).half(), w.to(dev), y.to(dev))
     with pytest.raises(TypeError):
         fp8rl.token_logprobs(x.to(dev), w.to(dev), y.long().to(dev))
+    with pytest.raises(TypeError):
+        fp8rl.token_logprobs(x.numpy, w.to(dev), y.to(dev))
     with pytest.raises(fp8rl.Fp8rlError):
         fp8rl.token_logprobs(x.to(dev)[:, :60].contiguous(), w.to(dev)[:, :60].contiguous(), y.to(dev))
 
