@@ -64,13 +64,14 @@ fp8rl_status vocab_backward(const VocabArgs& a, const DeviceState* ds, cudaStrea
 // Slices that give the dX product of `rows` x H enough tiles to fill the GPU.
 int vocab_dx_slices(int64_t rows, int64_t H, int64_t vc);
 
-// The same for up to kVocabFew rows whose hidden states fit in shared memory
-// as FP32 (vocab_few.cu): a read of the weights by plain FP32 arithmetic.
-constexpr int kVocabFew = 8;
+// The same for one row or two whose hidden states fit in shared memory as FP32
+// (vocab_few.cu): a read of the weights by plain FP32 arithmetic.  At 131072 x
+// 4096 it takes 159 us for one row and 163 for two (the tensor-core tiles take
+// 189 for up to 64); for four rows it took 195, for eight 299.
+constexpr int kVocabFew = 2;
 constexpr int kVocabFewBytes = 192 << 10;
-inline int vocab_few_rows(int rows) { return rows <= 2 ? rows : (rows <= 4 ? 4 : 8); }
 inline bool vocab_few(int rows, int64_t H) {
-  return rows <= kVocabFew && vocab_few_rows(rows) * H * 4 <= kVocabFewBytes;
+  return rows <= kVocabFew && rows * H * 4 <= kVocabFewBytes;
 }
 fp8rl_status vocab_forward_few(const VocabArgs& a, const DeviceState* ds, cudaStream_t stream);
 

@@ -105,10 +105,9 @@ struct Params {
   CUtensorMap g_mn, x_mn, dw_out;   // dW
   VocabArgs a;
   int x_rows[2];   // rows of the boxes of x_k; 0: nothing to load
-  int tn;          // stats, grad: columns of a tile, a multiple of 32 up to kTile
+  int tn;          // stats, grad: columns of a tile, a multiple of 32 (grad: 64) up to kTile
   int v_grad;      // first vocabulary column of the grad piece
   int n_grad;      // its column tiles (0: none)
-  __nv_bfloat16* g_row;   // the piece of G written
   int v_prod;      // first column of the piece whose products are formed
   int vc_prod;     // its columns
   int dx_tiles_n;  // column tiles of H when dX / dW are wanted, else 0
@@ -671,25 +670,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
               o[e] = *reinterpret_cast<const uint32_t*>(&b);
             }
             if (j.kind == kGrad) {
-              // BF16 boxes of 32 columns (64-byte swizzle); half a box at the
-              // end of a narrow tile is stored from the registers
+              // BF16 boxes of 32 columns (64-byte swizzle)
               const int col = col0 + c * 32;
-              if (hw - c * 32 >= 32) {
-                const uint32_t box = stg + c * (kBoxBytes / 2);
+              const uint32_t box = stg + c * (kBoxBytes / 2);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  st_shared_v4(box + (uint32_t)(lane * 64 + ((e ^ ((lane >> 1) & 3)) * 16)), o[e * 4],
-                               o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                  if (col < a.vc) tma_store_2d(&p.g_out, box, col, row0);
-                  bulk_commit();
-                }
-              } else if (col < a.vc) {
-                uint4* to = reinterpret_cast<uint4*>(p.g_row + (int64_t)row * a.vc + col);
-                to[0] = make_uint4(o[0], o[1], o[2], o[3]);
-                to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+              for (int e = 0; e < 4; ++e)
+                st_shared_v4(box + (uint32_t)(lane * 64 + ((e ^ ((lane >> 1) & 3)) * 16)), o[e * 4],
+                             o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                if (col < a.vc) tma_store_2d(&p.g_out, box, col, row0);
+                bulk_commit();
               }
             } else {
               // BF16 boxes of 64 columns (128-byte swizzle)
@@ -736,11 +728,10 @@ fp8rl_status map_bf16(CUtensorMap* m, const void* base, int64_t inner, int64_t r
                          (uint64_t)ld * 2, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B, what);
 }
 
-// X's boxes: the tile's 128 rows per CTA.  Where there is one row tile, only the
-// rows it has, to a multiple of 8: the copy engine takes about 2.3 cycles for
-// each 128-byte row, whether it holds anything or not, and with W's rows alone
-// it keeps up with HBM.  (What lies in shared memory instead belongs to rows
-// of the product that nobody reads.)
+// X's boxes: the tile's 128 rows per CTA; where there is one row tile, only the
+// rows it has, to a multiple of 8 (what lies in shared memory instead belongs to
+// rows of the product that nobody reads).  100 rows x 3000 x 100000 take 117.6
+// us, with whole boxes 141.
 fp8rl_status map_x(Params* p, const VocabArgs& a) {
   const int rows = a.lo_off + a.rows_cap;
   for (int r = 0; r < 2; ++r) {
@@ -823,19 +814,26 @@ int vocab_dx_slices(int64_t rows, int64_t H, int64_t vc) {
 namespace {
 
 // Columns of the head tiles (stats, grad) for `mt` row tiles x V columns on
-// `pairs` pairs of SMs: the width, a multiple of 32 from 64 on, whose rounds
+// `pairs` pairs of SMs: the width, in steps of `unit` from 64 on, whose rounds
 // take the least time, a round counted as its width plus 16 columns' worth of
-// overhead.  With many rounds that is the full width (and nothing else is
-// looked at from kNarrowTiles tiles on); with few, a narrower tile keeps the
-// last round from leaving most SMs idle: 32768 columns are 128 full tiles, two
-// rounds on 76 pairs, or two rounds of 224.
-constexpr int kNarrowTiles = 600, kNarrowest = 64;
+// overhead.  It is looked for
+//   - where full tiles would leave half of the pairs without one: 64 rows x
+//     4096 x 4096 with its gradient take 45.6 us instead of 51.3;
+//   - for the forward pass of one row tile, which waits for W: the last round
+//     then keeps every SM loading (100 x 3000 x 100000: 117.6 us instead of
+//     124.7; 64 x 2048 x 65536: 56.5 instead of 58.2).  With more row tiles, or
+//     for G, narrow tiles lost (400 x 1000 x 60000: 186.6 us instead of 175.8).
+constexpr int kFewTiles = 38, kNarrowTiles = 600, kNarrowest = 64;
+inline bool may_narrow(int64_t mt, int64_t V, bool fwd) {
+  return mt * tiles(V) <= kFewTiles || (fwd && mt == 1 && tiles(V) <= kNarrowTiles);
+}
 
-int head_tile(int64_t mt, int64_t V, int pairs) {
-  if (mt * tiles(V) > kNarrowTiles) return kTile;
+int head_tile(int64_t mt, int64_t V, int pairs, bool fwd) {
+  if (!may_narrow(mt, V, fwd)) return kTile;
+  const int unit = fwd ? 32 : 64;
   int best = kTile;
   int64_t cost = INT64_MAX;
-  for (int tn = kTile; tn >= kNarrowest; tn -= 32) {
+  for (int tn = kTile; tn >= kNarrowest; tn -= unit) {
     const int64_t rounds = (mt * ((V + tn - 1) / tn) + pairs - 1) / pairs;
     const int64_t c = rounds * (tn + 16);
     if (c < cost) {
@@ -852,12 +850,12 @@ int vocab_parts(const VocabArgs& a, const DeviceState* ds) {
   if (vocab_few(a.rows_cap, a.H)) return ds->sm_count;
   int pairs = 1;
   pairs_of<true>(ds, &pairs);
-  const int half = head_tile(a.rows_pad / kTile, a.V, pairs) / 2;
+  const int half = head_tile(a.rows_pad / kTile, a.V, pairs, true) / 2;
   return (a.V + half - 1) / half;
 }
 
 int64_t vocab_most_parts(int64_t rows, int64_t V) {
-  const bool narrow = tiles(std::max<int64_t>(rows, 1)) * tiles(V) <= kNarrowTiles;
+  const bool narrow = may_narrow(tiles(std::max<int64_t>(rows, 1)), V, true);
   const int64_t half = (narrow ? kNarrowest : kTile) / 2;
   return std::max<int64_t>((V + half - 1) / half, kMostSms);
 }
@@ -869,7 +867,7 @@ fp8rl_status vocab_forward(const VocabArgs& a, const DeviceState* ds, cudaStream
   int pairs = 0;
   fp8rl_status st = pairs_of<true>(ds, &pairs);
   if (st != FP8RL_OK) return st;
-  p.tn = head_tile(a.rows_pad / kTile, a.V, pairs);
+  p.tn = head_tile(a.rows_pad / kTile, a.V, pairs, true);
   p.early = a.rows_pad == kTile;
   if ((st = map_x(&p, a)) != FP8RL_OK) return st;
   if ((st = map_bf16(&p.w_k, a.w, a.H, a.V, a.ldw, p.tn / 2, "weight")) != FP8RL_OK) return st;
@@ -885,7 +883,7 @@ fp8rl_status vocab_backward(const VocabArgs& a, const DeviceState* ds, cudaStrea
   const int64_t mt = tiles(a.rows_pad), ht = tiles(a.H);
   int pairs = 0;
   if ((st = pairs_of<false>(ds, &pairs)) != FP8RL_OK) return st;
-  p.tn = pieces == 1 ? head_tile(mt, a.V, pairs) : kTile;
+  p.tn = pieces == 1 ? head_tile(mt, a.V, pairs, false) : kTile;
   if ((st = map_x(&p, a)) != FP8RL_OK) return st;
   if ((st = map_bf16(&p.w_k, a.w, a.H, a.V, a.ldw, p.tn / 2, "weight")) != FP8RL_OK) return st;
   if ((st = map_bf16(&p.x_mn, a.x, a.H, a.rows_pad, a.H, 64, "hidden")) != FP8RL_OK) return st;
@@ -923,7 +921,6 @@ fp8rl_status vocab_backward(const VocabArgs& a, const DeviceState* ds, cudaStrea
       // (to a multiple of 64 columns, zeros past the vocabulary: dX sums whole steps)
       const int64_t cols = (std::min<int64_t>(a.vc, a.V - p.v_grad) + kBK - 1) / kBK * kBK;
       p.n_grad = (int)((cols + p.tn - 1) / p.tn);
-      p.g_row = a.g[i & 1];
       p.g_out = g_out[i & 1];
       jobs += mt * p.n_grad;
     }
