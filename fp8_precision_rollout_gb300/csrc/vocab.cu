@@ -124,7 +124,8 @@ struct RowsArgs {
   int V, H, rows_per_cta;
   const __nv_bfloat16* hidden; // [T, H], row stride ldh
   int64_t ldh;
-  __nv_bfloat16* x;            // [rows_pad, H]
+  __nv_bfloat16* x;            // [rows_pad, H], row stride ldx
+  int64_t ldx;
   int32_t* map;
   int32_t* tgt;
   int32_t* n_rows;             // [0]: rows of the products; [1]: kept tokens
@@ -260,8 +261,8 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsArgs a) {
         x = make_uint4(0, 0, 0, 0);
         if (a.grad_hidden) reinterpret_cast<uint4*>(a.grad_hidden + (c0 + r) * a.H)[v] = x;
       }
-      reinterpret_cast<uint4*>(a.x + dst * a.H)[v] = x;
-      if (a.lo_off) reinterpret_cast<uint4*>(a.x + (dst + a.lo_off) * a.H)[v] = x;
+      reinterpret_cast<uint4*>(a.x + dst * a.ldx)[v] = x;
+      if (a.lo_off) reinterpret_cast<uint4*>(a.x + (dst + a.lo_off) * a.ldx)[v] = x;
     };
     if (ahead) {
 #pragma unroll
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const RowsArgs a) {
       const int64_t r = s < gap ? a.T + s : rows + (s - gap);
       if (s < gap && tid == 0) empty_row(a, r);
       for (int v = tid; v < vecs; v += kRowThreads)
-        reinterpret_cast<uint4*>(a.x + r * a.H)[v] = make_uint4(0, 0, 0, 0);
+        reinterpret_cast<uint4*>(a.x + r * a.ldx)[v] = make_uint4(0, 0, 0, 0);
     }
   }
   if (r1 == a.T && tid == 0) {
@@ -413,8 +414,8 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
 // a fixed order) -> grad_hidden rows of their tokens.  A read of dX and a write
 // of the gradient: 12.5 us for 3072 rows of 4096 in one slice.
 __global__ void __launch_bounds__(256)
-    scatter_kernel(const float* dx, const int32_t* n_rows, const int32_t* map, int H, int slices,
-                   int64_t slice_stride, __nv_bfloat16* grad_hidden) {
+    scatter_kernel(const float* dx, const int32_t* n_rows, const int32_t* map, int H, int64_t ldx,
+                   int slices, int64_t slice_stride, __nv_bfloat16* grad_hidden) {
   ptx::grid_dependency_wait();
   ptx::grid_dependents_launch();
   const int vecs = H / 8;
@@ -422,11 +423,11 @@ __global__ void __launch_bounds__(256)
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t c = i / vecs;
     const int v = (int)(i - c * vecs) * 8;
-    const float4* src = reinterpret_cast<const float4*>(dx + c * H + v);
+    const float4* src = reinterpret_cast<const float4*>(dx + c * ldx + v);
     float4 x = src[0], y = src[1];
 #pragma unroll 4
     for (int k = 1; k < slices; ++k) {
-      src = reinterpret_cast<const float4*>(dx + k * slice_stride + c * H + v);
+      src = reinterpret_cast<const float4*>(dx + k * slice_stride + c * ldx + v);
       const float4 x2 = src[0], y2 = src[1];
       x.x += x2.x; x.y += x2.y; x.z += x2.z; x.w += x2.w;
       y.x += y2.x; y.y += y2.y; y.z += y2.z; y.w += y2.w;
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(256)
 // consecutive float4.  Grid: x = pieces of a row, y = rows (strided).
 __global__ void __launch_bounds__(256)
     scatter_few_kernel(const float* dx, const int32_t* n_rows, const int32_t* map, int H,
-                       int slices, int64_t slice_stride, int lo_off, __nv_bfloat16* grad_hidden) {
+                       int64_t ldx, int slices, int64_t slice_stride, int lo_off, __nv_bfloat16* grad_hidden) {
   ptx::grid_dependency_wait();
   ptx::grid_dependents_launch();
   constexpr int kG = 8, kW = 32 / kG;
@@ -452,13 +453,13 @@ __global__ void __launch_bounds__(256)
   for (int c = blockIdx.y; c < n; c += gridDim.y) {
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (v < H) {
-      const float* src = dx + (int64_t)c * H + v;
+      const float* src = dx + (int64_t)c * ldx + v;
 #pragma unroll 4
       for (int k = group; k < slices; k += kG) {
         const float4 y = *reinterpret_cast<const float4*>(src + k * slice_stride);
         x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
         if (lo_off) {
-          const float4 z = *reinterpret_cast<const float4*>(src + k * slice_stride + (int64_t)lo_off * H);
+          const float4 z = *reinterpret_cast<const float4*>(src + k * slice_stride + (int64_t)lo_off * ldx);
           x.x += z.x; x.y += z.y; x.z += z.z; x.w += z.w;
         }
       }
@@ -500,6 +501,7 @@ fp8rl_status launch(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s
 struct Plan {
   int64_t rows = 0;        // tokens handled at once (forward: a piece of them)
   int64_t rows_pad = 0;
+  int64_t ldx = 0;         // row stride of the packed rows and of dX
   int64_t vc = 0;          // backward: vocabulary columns of a piece
   int slices = 1;          // backward: separate sums of dX
   size_t x, map, tgt, n, part, zt, lse, gcoef, g0, g1, dx, flags, ids, p, lp, bytes;
@@ -537,7 +539,8 @@ Plan make_plan(int64_t T, int64_t H, int64_t V, int64_t K, bool backward) {
     at = (size_t)round_up((int64_t)(at + bytes), 256);
     return here;
   };
-  pl.x = take((size_t)pl.rows_pad * H * 2);
+  pl.ldx = round_up(H, 64);
+  pl.x = take((size_t)pl.rows_pad * pl.ldx * 2);
   pl.map = take((size_t)pl.rows_pad * 4);
   pl.tgt = take((size_t)pl.rows_pad * 4);
   pl.n = take(256);
@@ -553,7 +556,7 @@ Plan make_plan(int64_t T, int64_t H, int64_t V, int64_t K, bool backward) {
     pl.gcoef = take((size_t)pl.rows_pad * 4);
     pl.g0 = take((size_t)pl.rows_pad * pl.vc * 2);
     pl.g1 = pieces > 1 ? take((size_t)pl.rows_pad * pl.vc * 2) : pl.g0;
-    pl.dx = take((size_t)pl.slices * pl.rows_pad * H * 4);
+    pl.dx = take((size_t)pl.slices * pl.rows_pad * pl.ldx * 4);
   }
   if (K) {
     pl.flags = take((size_t)pl.rows_pad * 4);
@@ -667,6 +670,7 @@ fp8rl_status pack_rows(const Call& c, const Plan& pl, const DeviceState* ds, int
   r.hidden = reinterpret_cast<const __nv_bfloat16*>(c.hidden) + t0 * c.ldh;
   r.ldh = c.ldh;
   r.x = reinterpret_cast<__nv_bfloat16*>(ws + pl.x);
+  r.ldx = pl.ldx;
   r.map = reinterpret_cast<int32_t*>(ws + pl.map);
   r.tgt = reinterpret_cast<int32_t*>(ws + pl.tgt);
   r.n_rows = reinterpret_cast<int32_t*>(ws + pl.n);
@@ -684,6 +688,7 @@ fp8rl_status pack_rows(const Call& c, const Plan& pl, const DeviceState* ds, int
   }
   r.status = ds->status;
   va->x = r.x;
+  va->ldx = pl.ldx;
   va->w = reinterpret_cast<const __nv_bfloat16*>(c.weight);
   va->ldw = c.ldw;
   va->H = (int)c.H;
@@ -773,13 +778,13 @@ fp8rl_status run_backward(const Call& c, float coef) {
     if (va.slices >= 8 || va.lo_off) {
       st = launch(scatter_few_kernel,
                   dim3((unsigned)((c.H / 4 + 31) / 32), (unsigned)std::min<int64_t>(c.T, 4096)), 256,
-                  c.stream, "scatter_few_kernel launch", va.dx, va.n_rows, va.map, (int)c.H,
-                  va.slices, (int64_t)va.rows_pad * c.H, va.lo_off, gh);
+                  c.stream, "scatter_few_kernel launch", va.dx, va.n_rows, va.map, (int)c.H, va.ldx,
+                  va.slices, va.rows_pad * va.ldx, va.lo_off, gh);
     } else {
       const int64_t ctas = (c.T * (c.H / 8) + 255) / 256;
       st = launch(scatter_kernel, dim3((unsigned)std::min<int64_t>(ctas, 8 * ds->sm_count)), 256,
-                  c.stream, "scatter_kernel launch", va.dx, va.n_rows, va.map, (int)c.H, va.slices,
-                  (int64_t)va.rows_pad * c.H, gh);
+                  c.stream, "scatter_kernel launch", va.dx, va.n_rows, va.map, (int)c.H, va.ldx,
+                  va.slices, va.rows_pad * va.ldx, gh);
     }
     if (st != FP8RL_OK) return st;
   }

@@ -19,7 +19,8 @@ constexpr int kVocabPad = 256;
 // token map[c]; tokens without a target are not in it.  n_rows (device) is
 // their number, at most rows_cap.
 struct VocabArgs {
-  const __nv_bfloat16* x;   // [rows_pad, H]
+  const __nv_bfloat16* x;   // [rows_pad, H], row stride ldx
+  int64_t ldx;              // a multiple of 64: rows begin on 128-byte lines
   const __nv_bfloat16* w;   // [V, H], row stride ldw
   int64_t ldw;
   int H, V;
@@ -47,7 +48,7 @@ struct VocabArgs {
   __nv_bfloat16* g[2];      // [rows_pad, vc] each: alternating pieces of G
   int vc;                   // columns of a piece, a multiple of kVocabPad
   int slices;               // dX: sums over this many parts of a piece
-  float* dx;                // [slices, rows_pad, H] FP32, or null
+  float* dx;                // [slices, rows_pad, H] FP32, row stride ldx, or null
   __nv_bfloat16* dw;        // [V, H], or null
   uint32_t* status;
 };

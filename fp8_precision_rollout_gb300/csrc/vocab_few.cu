@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const VocabArgs a) {
   for (int i = tid; i < NT * vecs; i += kThreads) {
     const int t = i / vecs, c = i - t * vecs;
     uint4 v = make_uint4(0, 0, 0, 0);
-    if (t < n) v = reinterpret_cast<const uint4*>(a.x + (int64_t)t * a.H)[c];
+    if (t < n) v = reinterpret_cast<const uint4*>(a.x + (int64_t)t * a.ldx)[c];
     xs[(t * 2) * vecs + c] = make_ulonglong2(pack2(v.x << 16, v.x & 0xFFFF0000u), pack2(v.y << 16, v.y & 0xFFFF0000u));
     xs[(t * 2 + 1) * vecs + c] = make_ulonglong2(pack2(v.z << 16, v.z & 0xFFFF0000u), pack2(v.w << 16, v.w & 0xFFFF0000u));
   }

@@ -738,7 +738,7 @@ fp8rl_status map_x(Params* p, const VocabArgs& a) {
     p->x_rows[r] = 128;
     if (a.rows_pad == kTile) p->x_rows[r] = std::min(128, std::max(0, (rows - 128 * r + 7) / 8 * 8));
     const fp8rl_status st =
-        map_bf16(&p->x_k[r], a.x, a.H, a.rows_pad, a.H, (uint32_t)std::max(8, p->x_rows[r]), "hidden");
+        map_bf16(&p->x_k[r], a.x, a.H, a.rows_pad, a.ldx, (uint32_t)std::max(8, p->x_rows[r]), "hidden");
     if (st != FP8RL_OK) return st;
   }
   return FP8RL_OK;
@@ -886,7 +886,7 @@ fp8rl_status vocab_backward(const VocabArgs& a, const DeviceState* ds, cudaStrea
   p.tn = pieces == 1 ? head_tile(mt, a.V, pairs, false) : kTile;
   if ((st = map_x(&p, a)) != FP8RL_OK) return st;
   if ((st = map_bf16(&p.w_k, a.w, a.H, a.V, a.ldw, p.tn / 2, "weight")) != FP8RL_OK) return st;
-  if ((st = map_bf16(&p.x_mn, a.x, a.H, a.rows_pad, a.H, 64, "hidden")) != FP8RL_OK) return st;
+  if ((st = map_bf16(&p.x_mn, a.x, a.H, a.rows_pad, a.ldx, 64, "hidden")) != FP8RL_OK) return st;
   if ((st = map_bf16(&p.w_mn, a.w, a.H, a.V, a.ldw, 64, "weight")) != FP8RL_OK) return st;
   CUtensorMap g_out[2], g_k[2], g_mn[2];
   for (int i = 0; i < 2; ++i) {
@@ -900,7 +900,7 @@ fp8rl_status vocab_backward(const VocabArgs& a, const DeviceState* ds, cudaStrea
   }
   if (a.dx) {
     if ((st = encode_tiled_2d(&p.dx_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.dx, (uint64_t)a.H,
-                              (uint64_t)a.slices * a.rows_pad, (uint64_t)a.H * 4, 32, 32,
+                              (uint64_t)a.slices * a.rows_pad, (uint64_t)a.ldx * 4, 32, 32,
                               CU_TENSOR_MAP_SWIZZLE_128B, "dX")) != FP8RL_OK)
       return st;
   } else {
