@@ -281,6 +281,54 @@ def test_pieces_of_tokens_and_of_the_vocabulary():
     _close16(gw[cols], want, tol, "grad_weight columns")
 
 
+def test_few_tokens_over_more_words_than_a_piece_of_g_holds():
+    """Two pieces of the vocabulary with several slices of dX each."""
+    dev = device()
+    t, h, v = 16, 64, 500003
+    x, w, y, g = _head(t, h, v, dev, seed=12)
+    y[3] = -1
+    y[4], y[5] = v - 1, 0
+    up = torch.randn(t, generator=g)
+    logp, lse = fp8rl.token_logprobs(x.to(dev), w.to(dev), y.to(dev))
+    gh, gw = fp8rl.token_logprobs_backward(x.to(dev), w.to(dev), y.to(dev), lse, up.to(dev))
+    torch.cuda.synchronize()
+    fp8rl.device_status(0)
+    _check_logp(x, w, y, logp, lse, 1.0)
+    d, kept = oracle.one_hot_targets(y.numpy(), v)
+    _check_grads(x, w, d, kept, up, -1.0, 1.0, gh, gw)
+
+
+@pytest.mark.parametrize("t", [2, 5])
+def test_offsets_past_32_bits(t):
+    """Weights and their gradient of more than 2^31 elements: targets and sampled
+    rows at the far end, against 64-bit products on the device."""
+    dev = device()
+    h, v = 16384, 140001
+    assert h * v > 2 ** 31
+    g = torch.Generator(device=dev).manual_seed(t)
+    w = torch.empty(v, h, dtype=torch.bfloat16, device=dev)
+    for i in range(0, v, 20000):
+        w[i:i + 20000] = torch.randn(min(20000, v - i), h, generator=g, device=dev).mul_(h ** -0.5).to(torch.bfloat16)
+    x = torch.randn(t, h, generator=g, device=dev).to(torch.bfloat16)
+    y = torch.tensor([v - 1, 131072, 5, 140000 - 3, v - 2][:t], dtype=torch.int32, device=dev)
+    up = torch.randn(t, generator=g, device=dev)
+    logp, lse = fp8rl.token_logprobs(x, w, y)
+    gh, gw = fp8rl.token_logprobs_backward(x, w, y, lse, up)
+    torch.cuda.synchronize()
+    fp8rl.device_status(0)
+    z = torch.cat([x.double() @ w[i:i + 20000].double().T for i in range(0, v, 20000)], 1)
+    ref = torch.log_softmax(z, 1).gather(1, y.long()[:, None])[:, 0]
+    assert float((logp.double() - ref).norm()) <= 1e-5 * float(ref.norm())
+    G = -torch.exp(z - torch.logsumexp(z, 1, keepdim=True))
+    G.scatter_add_(1, y.long()[:, None], torch.ones(t, 1, dtype=torch.float64, device=dev))
+    G *= up.double()[:, None]
+    rows = torch.tensor([0, 1, 131071, 131072, 139776, v - 3, v - 2, v - 1], device=dev)
+    want = G[:, rows].T @ x.double()
+    assert float((gw[rows].double() - want).norm()) <= 1.5 * 2.0 ** -8 * float(want.norm())
+    want = sum(G[:, i:i + 20000] @ w[i:i + 20000].double() for i in range(0, v, 20000))
+    assert float((gh.double() - want).norm()) <= 1.5 * 2.0 ** -8 * float(want.norm())
+
+
 def test_gradient_matches_differences_of_the_forward():
     """Central differences of the library's own forward along directions that
     BF16 represents: hidden states and weights are multiples of 2^-6 of at most
