@@ -514,70 +514,85 @@ def vocab_workspace_bytes(tokens: int, hidden_dim: int, vocab: int, top_k: int =
 # what is wrong with it.
 
 def _head(hidden, weight):
-    if not (isinstance(hidden, torch.Tensor) and isinstance(weight, torch.Tensor)
-            and hidden.is_cuda and weight.is_cuda and hidden.dtype is torch.bfloat16
-            and weight.dtype is torch.bfloat16 and hidden.dim() == 2 and weight.dim() == 2
+    dev = hidden.get_device() if isinstance(hidden, torch.Tensor) else -1
+    if not (dev >= 0 and isinstance(weight, torch.Tensor) and weight.get_device() == dev
+            and hidden.dtype is torch.bfloat16 and weight.dtype is torch.bfloat16
+            and hidden.dim() == 2 and weight.dim() == 2
             and hidden.stride(1) == 1 and weight.stride(1) == 1):
         _rowmajor(_dev(hidden, torch.bfloat16, "hidden"), "hidden")
         _rowmajor(_dev(weight, torch.bfloat16, "weight"), "weight")
+        raise ValueError("hidden and weight must be on one device")
     t, h = hidden.shape
     v, hw = weight.shape
     if h != hw:
         raise ValueError("hidden [tokens, hidden_dim] and weight [vocab, hidden_dim] must agree")
-    if weight.get_device() != hidden.get_device():
-        raise ValueError("hidden and weight must be on one device")
     # the stride of a single row says nothing (torch may report any value)
-    return t, h, v, (hidden.stride(0) if t > 1 else h), (weight.stride(0) if v > 1 else h)
+    return t, h, v, (hidden.stride(0) if t > 1 else h), (weight.stride(0) if v > 1 else h), dev
 
 
-def _dense(t, dtype, shape, like, name):
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape
-            and t.is_contiguous() and t.get_device() == like.get_device()):
+def _dense(t, dtype, shape, dev, name):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous() and t.get_device() == dev):
         _dev(t, dtype, name)
-        raise ValueError("%s must be a dense %s tensor on %s" % (name, list(shape), like.device))
+        raise ValueError("%s must be a dense %s tensor on cuda:%d" % (name, list(shape), dev))
     return t.data_ptr()
 
 
-def _head_stream(stream, like):
-    """(raw stream, whether it is the device's current one)."""
-    current = torch._C._cuda_getCurrentRawStream(like.get_device())
+def _head_stream(stream, dev):
     if stream is None:
-        return current, True
-    s = _stream(stream)
-    return s, s == current
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
 
 
-def _head_workspace(workspace, t, h, v, k, backward, like, stream, is_current):
+class _Scratch:
+    """Workspace of one call from torch's caching allocator, for the call's own
+    stream (a later allocation on that stream may have it once the call has
+    launched; work on other streams may not)."""
+
+    __slots__ = ("ptr", "size")
+
+    def __init__(self, size, stream):
+        self.ptr = None
+        self.ptr = torch._C._cuda_cudaCachingAllocator_raw_alloc(size, stream)
+        self.size = size
+
+    def __del__(self):
+        if self.ptr is not None:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(self.ptr)
+
+
+class _Given:
+    """The caller's workspace tensor."""
+
+    __slots__ = ("ptr", "size")
+
+    def __init__(self, workspace, dev):
+        _dev(workspace, torch.uint8, "workspace")
+        if not workspace.is_contiguous() or workspace.get_device() != dev:
+            raise ValueError("workspace must be a contiguous tensor on cuda:%d" % dev)
+        self.ptr, self.size = workspace.data_ptr(), workspace.numel()
+
+
+def _head_workspace(workspace, t, h, v, k, backward, dev, stream):
     if workspace is None:
-        need = load().fp8rl_vocab_workspace_bytes(t, h, v, k, backward)
-        workspace = torch.empty(max(1, need), dtype=torch.uint8, device=like.device)
-        if not is_current:
-            # freed on return: the allocator must know the stream that still uses it
-            workspace.record_stream(torch.cuda.ExternalStream(stream, device=like.device))
-        return workspace, need
-    return workspace, _workspace_size(workspace, like)
+        return _Scratch(load().fp8rl_vocab_workspace_bytes(t, h, v, k, backward) or 1, stream)
+    return _Given(workspace, dev)
 
 
-def _workspace_size(workspace, like):
-    _dev(workspace, torch.uint8, "workspace")
-    if not workspace.is_contiguous() or workspace.get_device() != like.get_device():
-        raise ValueError("workspace must be a contiguous tensor on %s" % like.device)
-    return workspace.numel()
-
-
-def _head_out(out, shape, dtype, like, name):
+def _head_out(out, dtype, shape, like, dev, name):
+    """(tensor, address) of an output: `out`, checked, or a new one."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    _dense(out, dtype, shape, like, name)
-    return out
+        out = torch.empty(shape, dtype=dtype, device=like.device)
+        return out, out.data_ptr()
+    return out, _dense(out, dtype, shape, dev, name)
 
 
-def _teacher_entries(teacher_ids, teacher_logits, t, like):
+def _teacher_entries(teacher_ids, teacher_logits, t, dev):
     if not isinstance(teacher_ids, torch.Tensor) or teacher_ids.dim() != 2:
         raise ValueError("teacher_ids must be a [tokens, top_k] tensor")
     k = teacher_ids.shape[1]
-    return (k, _dense(teacher_ids, torch.int32, (t, k), like, "teacher_ids"),
-            _dense(teacher_logits, torch.float32, (t, k), like, "teacher_logits"))
+    return (k, _dense(teacher_ids, torch.int32, (t, k), dev, "teacher_ids"),
+            _dense(teacher_logits, torch.float32, (t, k), dev, "teacher_logits"))
 
 
 def token_logprobs(hidden, weight, targets, logit_scale: float = 1.0,
@@ -585,25 +600,27 @@ def token_logprobs(hidden, weight, targets, logit_scale: float = 1.0,
                    workspace: Optional[torch.Tensor] = None, stream=None):
     """Log-probability of targets int32 [T] under softmax(logit_scale * hidden @ weight^T)
     (bf16 hidden [T, H], weight [V, H]) and the log-sum-exp, float32 [T] each:
-    (logp, lse).  Tokens with a negative target are left out (0, 0)."""
-    t, h, v, ldh, ldw = _head(hidden, weight)
-    tp = _dense(targets, torch.int32, (t,), hidden, "targets")
-    logp = _head_out(logp, (t,), torch.float32, hidden, "logp")
-    lse = _head_out(lse, (t,), torch.float32, hidden, "lse")
-    s, current = _head_stream(stream, hidden)
-    ws, size = _head_workspace(workspace, t, h, v, 0, 0, hidden, s, current)
+    (logp, lse).  Tokens with a negative target are left out (0, 0).  workspace:
+    a uint8 device tensor of vocab_workspace_bytes(T, H, V) bytes (allocated
+    for the call when None)."""
+    t, h, v, ldh, ldw, dev = _head(hidden, weight)
+    tp = _dense(targets, torch.int32, (t,), dev, "targets")
+    logp, op = _head_out(logp, torch.float32, (t,), hidden, dev, "logp")
+    lse, ep = _head_out(lse, torch.float32, (t,), hidden, dev, "lse")
+    s = _head_stream(stream, dev)
+    ws = _head_workspace(workspace, t, h, v, 0, 0, dev, s)
     _check(load().fp8rl_token_logprobs(hidden.data_ptr(), ldh, weight.data_ptr(), ldw, tp, t, h, v,
-                                       float(logit_scale), logp.data_ptr(), lse.data_ptr(), ws.data_ptr(),
-                                       size, s))
+                                       float(logit_scale), op, ep, ws.ptr, ws.size, s))
     return logp, lse
 
 
-def _head_gradients(hidden, weight, t, h, v, grad_hidden, grad_weight, need_hidden, need_weight):
+def _head_gradients(hidden, t, h, v, dev, grad_hidden, grad_weight, need_hidden, need_weight):
+    hp = wp = None
     if grad_hidden is not None or need_hidden:
-        grad_hidden = _head_out(grad_hidden, (t, h), torch.bfloat16, hidden, "grad_hidden")
+        grad_hidden, hp = _head_out(grad_hidden, torch.bfloat16, (t, h), hidden, dev, "grad_hidden")
     if grad_weight is not None or need_weight:
-        grad_weight = _head_out(grad_weight, (v, h), torch.bfloat16, hidden, "grad_weight")
-    return grad_hidden, grad_weight
+        grad_weight, wp = _head_out(grad_weight, torch.bfloat16, (v, h), hidden, dev, "grad_weight")
+    return grad_hidden, hp, grad_weight, wp
 
 
 def token_logprobs_backward(hidden, weight, targets, lse, grad_logp, logit_scale: float = 1.0,
@@ -614,18 +631,17 @@ def token_logprobs_backward(hidden, weight, targets, lse, grad_logp, logit_scale
     """Gradients (bf16 grad_hidden [T, H], grad_weight [V, H]) of
     sum(grad_logp * logp), with the lse token_logprobs returned.  An output
     that is neither given nor needed is not computed (None)."""
-    t, h, v, ldh, ldw = _head(hidden, weight)
-    tp = _dense(targets, torch.int32, (t,), hidden, "targets")
-    lp = _dense(lse, torch.float32, (t,), hidden, "lse")
-    gp = _dense(grad_logp, torch.float32, (t,), hidden, "grad_logp")
-    gh, gw = _head_gradients(hidden, weight, t, h, v, grad_hidden, grad_weight, need_hidden,
-                             need_weight)
-    s, current = _head_stream(stream, hidden)
-    ws, size = _head_workspace(workspace, t, h, v, 0, 1, hidden, s, current)
+    t, h, v, ldh, ldw, dev = _head(hidden, weight)
+    tp = _dense(targets, torch.int32, (t,), dev, "targets")
+    ep = _dense(lse, torch.float32, (t,), dev, "lse")
+    gp = _dense(grad_logp, torch.float32, (t,), dev, "grad_logp")
+    gh, hp, gw, wp = _head_gradients(hidden, t, h, v, dev, grad_hidden, grad_weight, need_hidden,
+                                     need_weight)
+    s = _head_stream(stream, dev)
+    ws = _head_workspace(workspace, t, h, v, 0, 1, dev, s)
     _check(load().fp8rl_token_logprobs_backward(
-        hidden.data_ptr(), ldh, weight.data_ptr(), ldw, tp, lp, gp, t, h, v, float(logit_scale),
-        None if gh is None else gh.data_ptr(), None if gw is None else gw.data_ptr(),
-        ws.data_ptr(), size, s))
+        hidden.data_ptr(), ldh, weight.data_ptr(), ldw, tp, ep, gp, t, h, v, float(logit_scale), hp,
+        wp, ws.ptr, ws.size, s))
     return gh, gw
 
 
@@ -636,15 +652,14 @@ def distill_topk(hidden, weight, teacher_ids, teacher_logits, logit_scale: float
     int32 [T, K], teacher_logits float32 [T, K]; id < 0 or logit -inf: absent)
     to the student softmax(logit_scale * hidden @ weight^T), and the student's
     log-sum-exp: (loss, lse).  Tokens without entries are left out (0, 0)."""
-    t, h, v, ldh, ldw = _head(hidden, weight)
-    k, ip, up = _teacher_entries(teacher_ids, teacher_logits, t, hidden)
-    loss = _head_out(loss, (t,), torch.float32, hidden, "loss")
-    lse = _head_out(lse, (t,), torch.float32, hidden, "lse")
-    s, current = _head_stream(stream, hidden)
-    ws, size = _head_workspace(workspace, t, h, v, k, 0, hidden, s, current)
+    t, h, v, ldh, ldw, dev = _head(hidden, weight)
+    k, ip, up = _teacher_entries(teacher_ids, teacher_logits, t, dev)
+    loss, op = _head_out(loss, torch.float32, (t,), hidden, dev, "loss")
+    lse, ep = _head_out(lse, torch.float32, (t,), hidden, dev, "lse")
+    s = _head_stream(stream, dev)
+    ws = _head_workspace(workspace, t, h, v, k, 0, dev, s)
     _check(load().fp8rl_distill_topk(hidden.data_ptr(), ldh, weight.data_ptr(), ldw, ip, up, k, t,
-                                     h, v, float(logit_scale), loss.data_ptr(), lse.data_ptr(),
-                                     ws.data_ptr(), size, s))
+                                     h, v, float(logit_scale), op, ep, ws.ptr, ws.size, s))
     return loss, lse
 
 
@@ -656,18 +671,17 @@ def distill_topk_backward(hidden, weight, teacher_ids, teacher_logits, lse, grad
     """Gradients (bf16 grad_hidden [T, H], grad_weight [V, H]) of
     sum(grad_loss * loss), with the lse distill_topk returned; outputs as in
     token_logprobs_backward."""
-    t, h, v, ldh, ldw = _head(hidden, weight)
-    k, ip, up = _teacher_entries(teacher_ids, teacher_logits, t, hidden)
-    lp = _dense(lse, torch.float32, (t,), hidden, "lse")
-    gp = _dense(grad_loss, torch.float32, (t,), hidden, "grad_loss")
-    gh, gw = _head_gradients(hidden, weight, t, h, v, grad_hidden, grad_weight, need_hidden,
-                             need_weight)
-    s, current = _head_stream(stream, hidden)
-    ws, size = _head_workspace(workspace, t, h, v, k, 1, hidden, s, current)
+    t, h, v, ldh, ldw, dev = _head(hidden, weight)
+    k, ip, up = _teacher_entries(teacher_ids, teacher_logits, t, dev)
+    ep = _dense(lse, torch.float32, (t,), dev, "lse")
+    gp = _dense(grad_loss, torch.float32, (t,), dev, "grad_loss")
+    gh, hp, gw, wp = _head_gradients(hidden, t, h, v, dev, grad_hidden, grad_weight, need_hidden,
+                                     need_weight)
+    s = _head_stream(stream, dev)
+    ws = _head_workspace(workspace, t, h, v, k, 1, dev, s)
     _check(load().fp8rl_distill_topk_backward(
-        hidden.data_ptr(), ldh, weight.data_ptr(), ldw, ip, up, k, lp, gp, t, h, v, float(logit_scale),
-        None if gh is None else gh.data_ptr(), None if gw is None else gw.data_ptr(),
-        ws.data_ptr(), size, s))
+        hidden.data_ptr(), ldh, weight.data_ptr(), ldw, ip, up, k, ep, gp, t, h, v,
+        float(logit_scale), hp, wp, ws.ptr, ws.size, s))
     return gh, gw
 
 

@@ -889,8 +889,8 @@ fp8rl_status vocab_backward(const VocabArgs& a, const DeviceState* ds, cudaStrea
   if ((st = map_bf16(&p.x_mn, a.x, a.H, a.rows_pad, a.ldx, 64, "hidden")) != FP8RL_OK) return st;
   if ((st = map_bf16(&p.w_mn, a.w, a.H, a.V, a.ldw, 64, "weight")) != FP8RL_OK) return st;
   CUtensorMap g_out[2], g_k[2], g_mn[2];
-  for (int i = 0; i < 2; ++i) {
-    const void* g = a.g[i] ? a.g[i] : a.g[0];
+  for (int i = 0; i < (pieces > 1 ? 2 : 1); ++i) {
+    const void* g = a.g[i];
     if ((st = encode_tiled_2d(&g_out[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g, (uint64_t)a.vc,
                               (uint64_t)a.rows_pad, (uint64_t)a.vc * 2, 32, 32,
                               CU_TENSOR_MAP_SWIZZLE_64B, "G")) != FP8RL_OK)
