@@ -415,9 +415,11 @@ fp8rl_status fp8rl_token_logprobs(const void* hidden, int64_t ldh, const void* w
  * respect to hidden and weight.  With q_tv = exp(z_tv - lse[t]):
  *   G_tv        = grad_logp[t] * logit_scale * ([v == targets[t]] - q_tv)
  *   grad_hidden = G weight        grad_weight = G^T hidden
- * The logits are computed again, piece of the vocabulary by piece; a piece's
- * G is held in BF16 (one rounding, 2^-9 relative; at most about 192 MB, or 256
- * columns), the sums over it are FP32, and each gradient is rounded to BF16
+ * The logits are computed again, piece of the vocabulary by piece.  A piece's
+ * G is held in BF16 (one rounding, half a step of 2^-8 relative at most; with
+ * up to 128 tokens as two BF16 numbers, the rounded value and the rest), for
+ * two pieces of at most about 192 MB, or 256 columns, each.  The sums over G
+ * are FP32 (in the order the sizes give), and each gradient is rounded to BF16
  * once.  Tokens left out get zero rows of grad_hidden and add nothing.
  *   lse          FP32 [tokens] as fp8rl_token_logprobs wrote it
  *   grad_logp    FP32 [tokens]
