@@ -107,7 +107,8 @@ struct Params {
   int x_rows[2];   // rows of the boxes of x_k; 0: nothing to load
   int tn;          // stats, grad: columns of a tile, a multiple of 32 (grad: 64) up to kTile
   int v_grad;      // first vocabulary column of the grad piece
-  int n_grad;      // its column tiles (0: none)
+  int n_head;      // stats: column tiles
+  int n_grad;      // grad: column tiles of the piece (0: none)
   int v_prod;      // first column of the piece whose products are formed
   int vc_prod;     // its columns
   int dx_tiles_n;  // column tiles of H when dX / dW are wanted, else 0
@@ -141,7 +142,7 @@ __device__ __forceinline__ Schedule make_schedule(const Params& p, int n, int c,
   s.np = np;
   s.mt = (max(n, kFwd ? 0 : 1) + kTile - 1) / kTile;
   if (kFwd) {
-    s.nstats = s.mt * ((p.a.V + p.tn - 1) / p.tn);
+    s.nstats = s.mt * p.n_head;
     return s;
   }
   // dX jobs sum over a whole slice and are the longest: they go first, dealt
@@ -185,19 +186,19 @@ __device__ __forceinline__ bool get_job(const Params& p, const Schedule& s, int 
     const int t = s.c + i * s.np;
     if (t >= s.nstats) return false;
     int m, nn;
-    band_tile(t, s.mt, (p.a.V + p.tn - 1) / p.tn, &m, &nn);
+    band_tile(t, s.mt, p.n_head, &m, &nn);
     *j = {kStats, h_steps, m * kTile, nn * p.tn, 0, 0};
     return true;
   }
   const int mine = s.per + (s.c < s.rem ? 1 : 0);
   if (i < mine) {
     const int t = s.c + i * s.np;
-    const int nn = t % p.dx_tiles_n;
-    const int m = (t / p.dx_tiles_n) % s.mt;
-    const int slice = t / (p.dx_tiles_n * s.mt);
-    const int all = (p.vc_prod + kBK - 1) / kBK;
-    const int k0 = (int)((int64_t)all * slice / s.slices);
-    const int k1 = (int)((int64_t)all * (slice + 1) / s.slices);
+    const int u = t / p.dx_tiles_n, nn = t - u * p.dx_tiles_n;
+    const int slice = s.mt == 1 ? u : u / s.mt, m = u - slice * s.mt;
+    // (steps x slices stays below 2^31: at most 2^24 steps, 76 slices)
+    const uint32_t all = (uint32_t)(p.vc_prod + kBK - 1) / kBK;
+    const int k0 = (int)(all * (uint32_t)slice / (uint32_t)s.slices);
+    const int k1 = (int)(all * (uint32_t)(slice + 1) / (uint32_t)s.slices);
     *j = {kDx, k1 - k0, m * kTile, nn * kTile, k0 * kBK, slice};
     return true;
   }
@@ -209,7 +210,7 @@ __device__ __forceinline__ bool get_job(const Params& p, const Schedule& s, int 
     t = s.early * (s.np - s.rem) + (k - (s.c >= s.rem ? s.early : 0)) * s.np + s.c;
   if (t >= s.nb) return false;
   if (t < s.ndw) {
-    const int nn = t % p.dw_tiles_n, m = t / p.dw_tiles_n;
+    const int m = t / p.dw_tiles_n, nn = t - m * p.dw_tiles_n;
     *j = {kDw, (max(n, 1) + kBK - 1) / kBK, m * kTile, nn * kTile, 0, 0};
   } else {
     int m, nn;
@@ -341,6 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   }
   grid_dependency_wait();
   grid_dependents_launch();
+  const int rows = *a.n_rows;      // on its way while the pair meets
   // both CTAs' barriers exist before either CTA's work refers to them
   __syncthreads();
   cluster_arrive();
@@ -350,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = st->tmem_base;
-  const int n = __shfl_sync(0xFFFFFFFFu, *a.n_rows, 0);   // warp-uniform to the compiler too
+  const int n = __shfl_sync(0xFFFFFFFFu, rows, 0);   // warp-uniform to the compiler too
   const Schedule sch = make_schedule<kFwd>(p, n, (int)(blockIdx.x >> 1), (int)(gridDim.x >> 1));
 
   if (warp == 0) {
@@ -871,7 +873,8 @@ fp8rl_status vocab_forward(const VocabArgs& a, const DeviceState* ds, cudaStream
   p.early = a.rows_pad == kTile;
   if ((st = map_x(&p, a)) != FP8RL_OK) return st;
   if ((st = map_bf16(&p.w_k, a.w, a.H, a.V, a.ldw, p.tn / 2, "weight")) != FP8RL_OK) return st;
-  return launch<true>(p, tiles(a.rows_cap) * ((a.V + p.tn - 1) / p.tn), ds, stream);
+  p.n_head = (a.V + p.tn - 1) / p.tn;
+  return launch<true>(p, tiles(a.rows_cap) * p.n_head, ds, stream);
 }
 
 fp8rl_status vocab_backward(const VocabArgs& a, const DeviceState* ds, cudaStream_t stream) {
