@@ -547,6 +547,10 @@ Plan make_plan(int64_t T, int64_t H, int64_t V, int64_t K, bool backward) {
   if (!backward) {
     pl.part = take((size_t)pl.rows_pad * parts * 8);
     pl.zt = take((size_t)pl.rows_pad * std::max<int64_t>(K, 1) * 4);
+  } else if (vocab_few_grad(T, H)) {
+    pl.lse = take((size_t)pl.rows_pad * 4);
+    pl.gcoef = take((size_t)pl.rows_pad * 4);
+    pl.dx = take((size_t)kMostSms * kVocabFew * pl.ldx * 4);
   } else {
     const int64_t most = std::max<int64_t>(kVocabPad, kGradBytes / (pl.rows_pad * 2) / kVocabPad * kVocabPad);
     const int64_t pieces = (V + most - 1) / most;
@@ -680,7 +684,7 @@ fp8rl_status pack_rows(const Call& c, const Plan& pl, const DeviceState* ds, int
     r.coef = coef;
     r.lse_c = reinterpret_cast<float*>(ws + pl.lse);
     r.gcoef_c = reinterpret_cast<float*>(ws + pl.gcoef);
-    r.lo_off = va->lo_off = lo_offset(rows);
+    r.lo_off = va->lo_off = vocab_few_grad(rows, c.H) ? 0 : lo_offset(rows);
     r.grad_hidden = reinterpret_cast<__nv_bfloat16*>(c.grad_hidden);
   } else {
     r.out0 = c.out + t0;
@@ -772,19 +776,27 @@ fp8rl_status run_backward(const Call& c, float coef) {
   va.slices = pl.slices;
   va.dx = c.grad_hidden ? reinterpret_cast<float*>(c.ws + pl.dx) : nullptr;
   va.dw = reinterpret_cast<__nv_bfloat16*>(c.grad_weight);
-  if ((st = vocab_backward(va, ds, c.stream)) != FP8RL_OK) return st;
+  int64_t slice_stride = (int64_t)va.rows_pad * va.ldx;
+  if (vocab_few_grad(c.T, c.H)) {
+    va.slices = ds->sm_count;
+    slice_stride = kVocabFew * va.ldx;
+    st = vocab_backward_few(va, ds, c.stream);
+  } else {
+    st = vocab_backward(va, ds, c.stream);
+  }
+  if (st != FP8RL_OK) return st;
   if (c.grad_hidden) {
     __nv_bfloat16* gh = reinterpret_cast<__nv_bfloat16*>(c.grad_hidden);
     if (va.slices >= 8 || va.lo_off) {
       st = launch(scatter_few_kernel,
                   dim3((unsigned)((c.H / 4 + 31) / 32), (unsigned)std::min<int64_t>(c.T, 4096)), 256,
                   c.stream, "scatter_few_kernel launch", va.dx, va.n_rows, va.map, (int)c.H, va.ldx,
-                  va.slices, va.rows_pad * va.ldx, va.lo_off, gh);
+                  va.slices, slice_stride, va.lo_off, gh);
     } else {
       const int64_t ctas = (c.T * (c.H / 8) + 255) / 256;
       st = launch(scatter_kernel, dim3((unsigned)std::min<int64_t>(ctas, 8 * ds->sm_count)), 256,
                   c.stream, "scatter_kernel launch", va.dx, va.n_rows, va.map, (int)c.H, va.ldx,
-                  va.slices, va.rows_pad * va.ldx, gh);
+                  va.slices, slice_stride, gh);
     }
     if (st != FP8RL_OK) return st;
   }

@@ -1,5 +1,6 @@
-// vocab_few.cu -- softmax partials and target logits of one row or two: the
-// log-probability of a token that has just been sampled.
+// vocab_few.cu -- softmax partials and target logits of one row or two (the
+// log-probability of a token that has just been sampled), and the gradient of as
+// few rows.
 //
 // The work is one read of the vocabulary weights (2 V H bytes; 1.07 GB and 158
 // us at 131072 x 4096 and the measured 6.79 TB/s) with 2 n FLOP per weight; it
@@ -42,6 +43,25 @@ __device__ __forceinline__ uint4 load_once(const uint4* p) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
+}
+
+// The warp's sums of kSums values (a power of two up to 32) by halving: lane l
+// ends with sum l / (32 / kSums) in z[0].
+template <int kSums>
+__device__ __forceinline__ void halve(float (&z)[kSums], int lane) {
+#pragma unroll
+  for (int o = 16, left = kSums; o; o >>= 1) {
+    if (left > 1) {
+      left >>= 1;
+#pragma unroll
+      for (int i = 0; i < left; ++i) {
+        const float keep = (lane & o) ? z[i + left] : z[i], give = (lane & o) ? z[i] : z[i + left];
+        z[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+      }
+    } else {
+      z[0] += __shfl_xor_sync(0xFFFFFFFFu, z[0], o);
+    }
+  }
 }
 
 template <int NT>
@@ -117,19 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const VocabArgs a) {
 #pragma unroll
       for (int i = 0; i < kRows; ++i)
         z[t * kRows + i] = __uint_as_float((uint32_t)acc[t][i]) + __uint_as_float((uint32_t)(acc[t][i] >> 32));
-#pragma unroll
-    for (int o = 16, left = kSums; o; o >>= 1) {
-      if (left > 1) {
-        left >>= 1;
-#pragma unroll
-        for (int i = 0; i < left; ++i) {
-          const float keep = (lane & o) ? z[i + left] : z[i], give = (lane & o) ? z[i] : z[i + left];
-          z[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
-        }
-      } else {
-        z[0] += __shfl_xor_sync(0xFFFFFFFFu, z[0], o);
-      }
-    }
+    halve<kSums>(z, lane);
     const int row = v + lr;
     if (mine && row < v1) {
       vocab_join(m, r, z[0], z[0] == -INFINITY ? -1.0f : 0.0f, k2);
@@ -156,6 +164,181 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const VocabArgs a) {
     for (int i = 1; i < kWarps; ++i) vocab_join(m, r, wm[i][tid], wr[i][tid], k2);
     a.part[(int64_t)blockIdx.x * a.rows_pad + tid] = make_float2(m, r);
   }
+}
+
+// The gradient of up to NT rows in one pass over the weights.  A weights row is
+// all that its G_tv, its row of dW and its share of dX need, so it is read once
+// and its row of dW is written: 4 V H bytes, where the tensor-core tiles read W
+// a second time for dX and pass G through memory.
+//
+// A group of warps as wide as a row (16 bytes a thread) takes a contiguous
+// range of the vocabulary, four weights rows at a time, with the next four
+// loading.  Each thread keeps its 8 columns of the n rows and of dX in
+// registers; the 4 n logits are summed over the group through shared memory,
+// 4 n threads turn them into G (FP32, not rounded), and the group goes on to dW
+// and dX.  Each CTA leaves one FP32 slice of dX, the groups' sums added in order.
+template <int NT>
+__global__ void __launch_bounds__(kThreads, 1) few_grad_kernel(const VocabArgs a) {
+  extern __shared__ float dxs[];           // [NT][H]
+  __shared__ float red[2][kWarps][NT * kRows], gs[2][kWarps][NT * kRows];
+  __shared__ int32_t sids[NT][kMaxK];
+  __shared__ float sp[NT][kMaxK];
+  ptx::grid_dependency_wait();
+  ptx::grid_dependents_launch();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n = min(*a.n_rows, NT);
+  const int vecs = a.H / 8, K = max(a.K, 1);
+  const int gw = (vecs + 31) >> 5, groups = kWarps / gw;      // warps of a group
+  const int g = warp / gw, gwarp = warp - g * gw, c = gwarp * 32 + lane;
+  const bool on = g < groups, mine = on && c < vecs;
+  for (int i = tid; i < n * K; i += kThreads) {
+    const int t = i / K, k = i - t * K;
+    sids[t][k] = a.K ? a.ids[(int64_t)a.map[t] * K + k] : a.tgt[t];
+    sp[t][k] = a.K ? a.p[(int64_t)a.map[t] * K + k] : 1.0f;
+  }
+  // this thread's columns of the rows, and of dX
+  uint64_t h[NT][4], dx[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (mine && t < n) x = reinterpret_cast<const uint4*>(a.x + (int64_t)t * a.ldx)[c];
+    h[t][0] = pack2(x.x << 16, x.x & 0xFFFF0000u);
+    h[t][1] = pack2(x.y << 16, x.y & 0xFFFF0000u);
+    h[t][2] = pack2(x.z << 16, x.z & 0xFFFF0000u);
+    h[t][3] = pack2(x.w << 16, x.w & 0xFFFF0000u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dx[t][i] = 0;
+  }
+  // the threads that turn logits into G: one per (row t, weights row lr)
+  const int lt = c / kRows, lr = c % kRows;
+  const bool turns = on && gwarp == 0 && lt < n;
+  const float k2 = a.scale * 1.4426950408889634f;
+  const float nl = turns ? -a.lse[lt] * 1.4426950408889634f : 0.0f, gc = turns ? a.gcoef[lt] : 0.0f;
+  int cur = 0;
+  __syncthreads();
+
+  const int64_t ng = (int64_t)gridDim.x * groups, gi = (int64_t)blockIdx.x * groups + g;
+  const int v0 = on ? (int)(a.V * gi / ng) : 0, v1 = on ? (int)(a.V * (gi + 1) / ng) : 0;
+  // one barrier per group (ids 1..), or none where the group is a warp
+  const auto meet = [&] {
+    __syncwarp();
+    if (gw > 1)
+      asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(gw * 32) : "memory");
+  };
+  uint4 nx[kRows];
+  const auto load = [&](int v) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      nx[i] = make_uint4(0, 0, 0, 0);
+      if (mine && v + i < v1)
+        nx[i] = load_once(reinterpret_cast<const uint4*>(a.w + (int64_t)(v + i) * a.ldw) + c);
+    }
+  };
+  load(v0);
+  int buf = 0;
+  for (int v = v0; v < v1; v += kRows, buf ^= 1) {
+    uint4 q[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) q[i] = nx[i];
+    load(v + kRows);
+    float z[NT * kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const uint64_t w0 = pack2(q[i].x << 16, q[i].x & 0xFFFF0000u), w1 = pack2(q[i].y << 16, q[i].y & 0xFFFF0000u);
+      const uint64_t w2 = pack2(q[i].z << 16, q[i].z & 0xFFFF0000u), w3 = pack2(q[i].w << 16, q[i].w & 0xFFFF0000u);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        uint64_t s = 0;
+        fma2(s, w0, h[t][0]);
+        fma2(s, w1, h[t][1]);
+        fma2(s, w2, h[t][2]);
+        fma2(s, w3, h[t][3]);
+        z[t * kRows + i] = __uint_as_float((uint32_t)s) + __uint_as_float((uint32_t)(s >> 32));
+      }
+    }
+    halve<NT * kRows>(z, lane);
+    constexpr int kDup = 32 / (NT * kRows);
+    if (lane % kDup == 0) red[buf][warp][lane / kDup] = z[0];
+    meet();
+    if (turns) {
+      float s = 0.0f;
+      for (int i = 0; i < gw; ++i) s += red[buf][warp + i][c];
+      float f = exp2f(fmaf(s, k2, nl));
+      const int row = v + lr;
+      while (cur < K && sids[lt][cur] < row) ++cur;
+      for (; cur < K && sids[lt][cur] == row; ++cur) f -= sp[lt][cur];
+      gs[buf][g][c] = gc * f;
+    } else if (on && gwarp == 0 && c < NT * kRows) {
+      gs[buf][g][c] = 0.0f;
+    }
+    meet();
+    // (the two buffers alternate: a warp is at most one meeting ahead of the
+    // slowest, and writes the other buffer then)
+    if (mine) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const uint64_t w[4] = {pack2(q[i].x << 16, q[i].x & 0xFFFF0000u), pack2(q[i].y << 16, q[i].y & 0xFFFF0000u),
+                               pack2(q[i].z << 16, q[i].z & 0xFFFF0000u), pack2(q[i].w << 16, q[i].w & 0xFFFF0000u)};
+        uint64_t d[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const uint32_t gt = __float_as_uint(gs[buf][g][t * kRows + i]);
+          const uint64_t gg = pack2(gt, gt);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            fma2(d[e], gg, h[t][e]);
+            // (a row past the range is zero and so is its share)
+            fma2(dx[t][e], gg, w[e]);
+          }
+        }
+        if (a.dw && v + i < v1) {
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float((uint32_t)d[e]),
+                                                           __uint_as_float((uint32_t)(d[e] >> 32)));
+            o[e] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          reinterpret_cast<uint4*>(a.dw + (int64_t)(v + i) * a.H)[c] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+    }
+  }
+  if (!a.dx) return;
+  for (int k = 0; k < groups; ++k) {
+    if (mine && g == k) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float2* at = reinterpret_cast<float2*>(dxs + (int64_t)t * a.H + c * 8 + e * 2);
+          float2 s = k ? *at : make_float2(0.0f, 0.0f);
+          s.x += __uint_as_float((uint32_t)dx[t][e]);
+          s.y += __uint_as_float((uint32_t)(dx[t][e] >> 32));
+          *at = s;
+        }
+    }
+    __syncthreads();
+  }
+  for (int i = tid; i < n * a.H; i += kThreads) {
+    const int t = i / a.H, col = i - t * a.H;
+    a.dx[((int64_t)blockIdx.x * kVocabFew + t) * a.ldx + col] = dxs[(int64_t)t * a.H + col];
+  }
+}
+
+template <int NT>
+fp8rl_status launch_few_grad(const VocabArgs& a, const DeviceState* ds, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ds->sm_count);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)NT * a.H * 4;      // at most 32 KB, under the default limit
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_check(cudaLaunchKernelEx(&cfg, few_grad_kernel<NT>, a), "few_grad_kernel launch");
 }
 
 template <int NT>
@@ -186,6 +369,10 @@ fp8rl_status launch_few(const VocabArgs& a, const DeviceState* ds, cudaStream_t 
 }
 
 }  // namespace
+
+fp8rl_status vocab_backward_few(const VocabArgs& a, const DeviceState* ds, cudaStream_t stream) {
+  return a.rows_cap == 1 ? launch_few_grad<1>(a, ds, stream) : launch_few_grad<2>(a, ds, stream);
+}
 
 fp8rl_status vocab_forward_few(const VocabArgs& a, const DeviceState* ds, cudaStream_t stream) {
   return a.rows_cap == 1 ? launch_few<1>(a, ds, stream) : launch_few<2>(a, ds, stream);

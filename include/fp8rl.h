@@ -420,7 +420,10 @@ fp8rl_status fp8rl_token_logprobs(const void* hidden, int64_t ldh, const void* w
  * up to 128 tokens as two BF16 numbers, the rounded value and the rest), for
  * two pieces of at most about 192 MB, or 256 columns, each.  The sums over G
  * are FP32 (in the order the sizes give), and each gradient is rounded to BF16
- * once.  Tokens left out get zero rows of grad_hidden and add nothing.
+ * once.  (One token or two, hidden_dim <= 4096: in one pass over the weights,
+ * with G in FP32.)  A nearly certain token's gradient is as exact as its FP32
+ * lse says how certain it is.  Tokens left out get zero rows of grad_hidden and
+ * add nothing.
  *   lse          FP32 [tokens] as fp8rl_token_logprobs wrote it
  *   grad_logp    FP32 [tokens]
  *   grad_hidden  BF16 [tokens, hidden_dim] dense, 16-byte aligned, or NULL

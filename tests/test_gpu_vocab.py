@@ -214,7 +214,8 @@ def test_distillation_matches_the_oracle(t, h, v, k, mask):
     _check_grads(x, w, dense, kept, up, 1.0, scale, gh.view.view(t, h), gw.view.view(v, h))
 
 
-@pytest.mark.parametrize("t,h,v,k", [(8, 4096, 3001, 0), (5, 72, 1001, 9), (8, 256, 129, 256),
+@pytest.mark.parametrize("t,h,v,k", [(1, 4096, 3001, 5), (2, 4096, 513, 0), (2, 4104, 700, 40),
+                                     (2, 1000, 3, 2), (1, 2056, 20000, 0), (8, 4096, 3001, 0), (5, 72, 1001, 9), (8, 256, 129, 256),
                                      (70, 264, 33000, 0), (128, 64, 32768, 12), (130, 128, 16500, 3),
                                      (389, 136, 20011, 0), (600, 64, 50021, 0), (600, 72, 40000, 70),
                                      (1100, 128, 9000, 0), (4500, 64, 3000, 0)])
