@@ -20,7 +20,8 @@
 //   rows_kernel      packs the tokens that have a target into consecutive
 //                    rows: a left-out token costs no products, and what its
 //                    hidden state holds (NaN included) reaches nothing;
-//   the products     (vocab_gemm.cu), over pieces of the vocabulary;
+//   the products     (vocab_gemm.cu; vocab_few.cu for one token or two), over
+//                    pieces of the vocabulary;
 //   combine_kernel / scatter_kernel   outputs per token.
 #include <algorithm>
 #include <climits>
